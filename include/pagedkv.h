@@ -48,7 +48,11 @@ typedef enum {
   PKV_ERR_TIMEOUT = -4       /* a kernel's bounded wait ran out (pkv_poll_device_error) */
 } pkv_status;
 
-typedef enum { PKV_BF16 = 0, PKV_INT8 = 1 } pkv_kv_dtype;
+typedef enum { PKV_BF16 = 0, PKV_INT8 = 1, PKV_INT4 = 4 } pkv_kv_dtype;
+
+/* Bytes of one (page, KV head) slab of a PKV_INT4 pool: 16 vectors of 128
+ * 4-bit codes, then their fp16 scales (see pkv_pool). */
+#define PKV_INT4_SLAB_BYTES 1152
 
 /*
  * One paged KV pool (TileInfer.jl "Performance" page: "the pool", read
@@ -59,6 +63,16 @@ typedef enum { PKV_BF16 = 0, PKV_INT8 = 1 } pkv_kv_dtype;
  * [page_size] ("INT8 KV cache": one scale per cached vector); for PKV_BF16
  * they must be NULL.  k and v must be 16-byte aligned.  Position p of
  * sequence b lives in page block_table[b][p / page_size], slot p % page_size.
+ *
+ * PKV_INT4: k and v are [num_pages][num_kv_heads] slabs of 1,152 bytes, codes
+ * and scales together (k_scale and v_scale must be NULL), so that a page of a
+ * head is one contiguous copy.  In a slab, group g is channels 32 g .. 32 g + 31:
+ *   bytes 0 .. 1023     codes: group g of slot t at 256 g + 16 t, 16 bytes;
+ *                       byte j holds channel 32 g + 2 j in its low and channel
+ *                       32 g + 2 j + 1 in its high four bits, each as code + 8
+ *                       (code -7 .. 7);
+ *   bytes 1024 .. 1151  IEEE fp16 scales [slot 16][group 4].
+ * A cached channel's value is code * scale: 4.5 bits per channel.
  */
 typedef struct {
   void* k;
@@ -84,14 +98,19 @@ typedef struct {
  *  seq_lens      int32 [batch] cached positions of each sequence AFTER this
  *                append; new row i of sequence b goes to position
  *                seq_lens[b] - n_b + i, n_b = cu_new[b+1] - cu_new[b].
- *  k_smooth      fp32 [128] per-channel key weight (> 0) or NULL.  INT8
- *                pools only: keys are divided by it before quantisation.
+ *  k_smooth      fp32 [128] per-channel key weight (> 0) or NULL.  INT8 and
+ *                INT4 pools: keys are divided by it (fp32) before quantisation.
  *                Must be NULL for bf16 pools.
  *
  * bf16 pools: the vectors are copied bit for bit.  INT8 pools: per vector x
  * (fp32; k / w for smoothed keys), scale = max|x| / 127 in fp32, code =
  * round-half-even(x / scale) as an IEEE fp32 quotient, clamped to +-127; an
- * all-zero vector stores scale 0 and codes 0.  Slots not named are left
+ * all-zero vector stores scale 0 and codes 0.  INT4 pools: per group of 32
+ * channels, scale = max|x| / 7 (IEEE fp32 quotient, at most 65504) rounded to
+ * fp16, code = round-half-even(x / scale) as an IEEE fp32 quotient by the
+ * rounded scale, clamped to +-7 (so |x| beyond 458,528 saturates); a scale that
+ * rounds to 0 stores codes 0; a group that holds a NaN or an infinity stores
+ * a NaN scale and codes 0, and reads back as NaN.  Slots not named are left
  * untouched.  num_tokens == 0 launches nothing and returns PKV_OK.
  */
 pkv_status pkv_kv_append(const pkv_pool* pool, const void* k_new, const void* v_new,
@@ -371,6 +390,82 @@ pkv_status pkv_qkv_norm_rope_append(const pkv_pool* pool, const void* qkv, int32
                                     const float* rope_sin, int32_t max_pos, const int32_t* cu_new,
                                     int32_t batch, const int32_t* block_table, int32_t max_pages,
                                     const int32_t* seq_lens, void* q_out, void* stream);
+
+/*
+ * kv_unpack -- the cached positions of a quantised pool as bf16 pages: what
+ * lets pkv_paged_attn_prefill, which reads bf16 pools, run a chunk against a
+ * prefix held in 4 or 8 bits.  For every sequence b, KV head and position
+ * starts[b] <= p < seq_lens[b], K and V of position p (page
+ * src_block_table[b][p / 16] of src) are written to slot p % 16 of page
+ * dst_block_table[b][p / 16] of dst: bf16(code * scale) for V,
+ * bf16((code * scale) * k_smooth) for K, each product rounded to fp32.
+ *
+ *  src          PKV_INT4 or PKV_INT8 pool (PKV_ERR_UNSUPPORTED for bf16);
+ *               dst a bf16 pool with as many KV heads, in other memory.
+ *  src_block_table, dst_block_table  int32 [batch][src_max_pages] and
+ *               [batch][dst_max_pages]; entries of pages that hold no position
+ *               of the range are not read, so dst may be a small staging pool.
+ *  starts       int32 [batch] or NULL (0): the first position of each
+ *               sequence, e.g. the positions that an earlier call has unpacked.
+ *  seq_lens     int32 [batch]; max_seq_len (host) >= every seq_lens[b] and
+ *               <= 16 times either table's width.
+ *  k_smooth     the fp32 [128] weight given to kv_append, or NULL.
+ * Slots outside the range are left as they were; a sequence with starts[b] >=
+ * seq_lens[b] is left out.  A length outside 0 .. max_seq_len, a negative
+ * start or a page id outside its pool is skipped and flagged for
+ * pkv_poll_device_error.
+ */
+pkv_status pkv_kv_unpack(const pkv_pool* src, const pkv_pool* dst, int32_t batch,
+                         const int32_t* src_block_table, int32_t src_max_pages,
+                         const int32_t* dst_block_table, int32_t dst_max_pages,
+                         const int32_t* starts, const int32_t* seq_lens, int32_t max_seq_len,
+                         const float* k_smooth, void* stream);
+
+/*
+ * page_tables -- the step's block tables, lengths and slot map, built on the
+ * GPU from the requests' lengths: what a serving loop that never returns to
+ * the host (a captured graph of decode steps, for one) calls before
+ * pkv_kv_append.  Free pages wait in a ring: request b takes the pages its new
+ * tokens need from the front, in the order of the requests; an ended request's
+ * pages go to the back.
+ *
+ *  seq_lens      int32 [batch] cached positions before the step.
+ *  new_lens      int32 [batch] tokens each request appends (0: none); negative:
+ *                the request has ended, its ceil(len / 16) pages are freed.
+ *  free_ring     int32 [ring_capacity] page ids, in and out: ring_state[1] free
+ *                pages from index ring_state[0] on, wrapping round.  The pages
+ *                held and free together must fit ring_capacity (num_pages
+ *                always does).
+ *  ring_state    int32 [2]: index of the first free page, number of them.
+ *  block_table   int32 [batch][max_pages], in and out: the pages a request
+ *                takes are written behind its ceil(len / 16) pages; all other
+ *                entries (an ended request's too) are left as they were.
+ *  seq_lens_out  int32 [batch]: positions after the step, 0 for an ended one.
+ *  cu_new        int32 [batch + 1]: prefix sums of the new tokens, as
+ *                pkv_kv_append takes them.
+ *  page_offsets  int32 [2][batch + 1]: prefix sums of the pages taken and of
+ *                the pages freed.
+ *  slot_map      int32 [slot_capacity] or NULL: page * 16 + slot of every new
+ *                token, in the order of cu_new; entries behind the last token
+ *                are left as they were.
+ *  ring_state_out int32 [2]: the ring after the step.
+ * seq_lens_out may be seq_lens and ring_state_out may be ring_state (the state
+ * of a loop, updated in place); otherwise no two arrays may overlap.
+ *
+ * All or nothing: if the ring is too short for what is asked, a length is
+ * negative or passes max_pages * 16, the tokens pass slot_capacity or 2^31 - 1,
+ * or the ring's state is not one, no page moves: seq_lens_out and
+ * ring_state_out repeat their inputs, cu_new and page_offsets are 0 (the
+ * step's append then writes nothing) and pkv_poll_device_error reports
+ * PKV_ERR_INVALID.  A page id outside 0 .. num_pages - 1 in the ring or the
+ * table is flagged too; its slots are -1.  batch == 0 launches nothing.
+ */
+pkv_status pkv_page_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t batch,
+                           int32_t* free_ring, int32_t ring_capacity, const int32_t* ring_state,
+                           int32_t num_pages, int32_t* block_table, int32_t max_pages,
+                           int32_t* seq_lens_out, int32_t* cu_new, int32_t* page_offsets,
+                           int32_t* slot_map, int32_t slot_capacity, int32_t* ring_state_out,
+                           void* stream);
 
 /*
  * Synchronises the stream, then reports and clears the device-side error

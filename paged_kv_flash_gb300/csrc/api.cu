@@ -64,7 +64,7 @@ pkv_status check_pool(const pkv_pool* pool) {
     return PKV_ERR_INVALID;
   if (pool->num_pages <= 0 || pool->num_kv_heads <= 0) return PKV_ERR_INVALID;
   if (!aligned(pool->k, 16) || !aligned(pool->v, 16)) return PKV_ERR_INVALID;
-  if (pool->dtype == PKV_BF16) {
+  if (pool->dtype == PKV_BF16 || pool->dtype == PKV_INT4) {   // INT4 scales lie in the slabs
     if (pool->k_scale || pool->v_scale) return PKV_ERR_INVALID;
   } else if (pool->dtype == PKV_INT8) {
     if (!pool->k_scale || !pool->v_scale) return PKV_ERR_INVALID;
@@ -236,8 +236,7 @@ pkv_status pkv_kv_append(const pkv_pool* pool, const void* k_new, const void* v_
   pkv_host::AppendLaunch a{pool->k, pool->v, pool->k_scale, pool->v_scale, pool->num_pages,
                            pool->num_kv_heads, k_new, v_new, num_tokens, cu_new, batch,
                            block_table, max_pages, seq_lens, k_smooth};
-  return cuda_status(pkv_host::launch_append(a, pool->dtype == PKV_INT8,
-                                             static_cast<cudaStream_t>(stream)));
+  return cuda_status(pkv_host::launch_append(a, pool->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_decode_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
@@ -257,6 +256,59 @@ pkv_status pkv_decode_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_he
   return PKV_OK;
 }
 
+pkv_status pkv_kv_unpack(const pkv_pool* src, const pkv_pool* dst, int32_t batch,
+                         const int32_t* src_block_table, int32_t src_max_pages,
+                         const int32_t* dst_block_table, int32_t dst_max_pages,
+                         const int32_t* starts, const int32_t* seq_lens, int32_t max_seq_len,
+                         const float* k_smooth, void* stream) {
+  pkv_status st = check_pool(src);
+  if (st != PKV_OK) return st;
+  st = check_pool(dst);
+  if (st != PKV_OK) return st;
+  if (dst->dtype != PKV_BF16 || dst->num_kv_heads != src->num_kv_heads || batch < 0 ||
+      src_max_pages <= 0 || dst_max_pages <= 0 || max_seq_len < 0 ||
+      (long long)max_seq_len >
+          (long long)std::min(src_max_pages, dst_max_pages) * pkv::kPageSize)
+    return PKV_ERR_INVALID;
+  if (src->dtype == PKV_BF16) return PKV_ERR_UNSUPPORTED;
+  if (batch == 0 || max_seq_len == 0) return PKV_OK;
+  if (!src_block_table || !dst_block_table || !seq_lens) return PKV_ERR_INVALID;
+  if (k_smooth && !aligned(k_smooth, 16)) return PKV_ERR_INVALID;
+  if (batch > 65535 ||
+      ((long long)max_seq_len / pkv::kPageSize + 1) * src->num_kv_heads > 2147483647ll - 64)
+    return PKV_ERR_UNSUPPORTED;
+  pkv_host::UnpackLaunch a{src->k,          src->v,          src->k_scale,    src->v_scale,
+                           src->num_pages,  src->num_kv_heads, dst->k,        dst->v,
+                           dst->num_pages,  batch,           src_block_table, src_max_pages,
+                           dst_block_table, dst_max_pages,   starts,          seq_lens,
+                           max_seq_len,     k_smooth};
+  return cuda_status(pkv_host::launch_unpack(a, src->dtype == PKV_INT4,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_page_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t batch,
+                           int32_t* free_ring, int32_t ring_capacity, const int32_t* ring_state,
+                           int32_t num_pages, int32_t* block_table, int32_t max_pages,
+                           int32_t* seq_lens_out, int32_t* cu_new, int32_t* page_offsets,
+                           int32_t* slot_map, int32_t slot_capacity, int32_t* ring_state_out,
+                           void* stream) {
+  // a slot is page * 16 + slot in an int32; positions are int32 too
+  if (batch < 0 || ring_capacity <= 0 || num_pages <= 0 || max_pages <= 0 || slot_capacity < 0)
+    return PKV_ERR_INVALID;
+  if (num_pages > 2147483647 / pkv::kPageSize || max_pages > 2147483647 / pkv::kPageSize ||
+      batch == 2147483647)
+    return PKV_ERR_UNSUPPORTED;
+  if (batch == 0) return PKV_OK;
+  if (!seq_lens || !new_lens || !free_ring || !ring_state || !block_table || !seq_lens_out ||
+      !cu_new || !page_offsets || !ring_state_out || (!slot_map && slot_capacity > 0))
+    return PKV_ERR_INVALID;
+  pkv_host::TablesLaunch a{seq_lens,     new_lens,     batch,    free_ring,    ring_capacity,
+                           ring_state,   num_pages,    block_table, max_pages, seq_lens_out,
+                           cu_new,       page_offsets, page_offsets + (size_t)batch + 1,
+                           slot_map,     slot_capacity, ring_state_out};
+  return cuda_status(pkv_host::launch_tables(a, static_cast<cudaStream_t>(stream)));
+}
+
 static pkv_status decode_call(const pkv_pool* pool, const void* q, int32_t batch,
                               int32_t num_q_heads, const int32_t* block_table, int32_t max_pages,
                               const int32_t* seq_lens, int32_t max_seq_len, float softmax_scale,
@@ -269,7 +321,8 @@ static pkv_status decode_call(const pkv_pool* pool, const void* q, int32_t batch
       max_seq_len < 0 || (long long)max_seq_len > (long long)max_pages * pkv::kPageSize ||
       num_splits < 0 || !std::isfinite(softmax_scale))
     return PKV_ERR_INVALID;
-  if (!pkv_host::decode_supports_group(num_q_heads / pool->num_kv_heads))
+  if (pool->dtype == PKV_INT4 ||
+      !pkv_host::decode_supports_group(num_q_heads / pool->num_kv_heads))
     return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
   if (!q || !block_table || !seq_lens || !out) return PKV_ERR_INVALID;
@@ -342,7 +395,8 @@ pkv_status pkv_paged_attn_decode_noalloc(const pkv_pool* pool, const void* q, in
       max_seq_len < 0 || (long long)max_seq_len > (long long)max_pages * pkv::kPageSize ||
       num_splits < 0 || !std::isfinite(softmax_scale))
     return PKV_ERR_INVALID;
-  if (!pkv_host::decode_supports_group(num_q_heads / pool->num_kv_heads))
+  if (pool->dtype == PKV_INT4 ||
+      !pkv_host::decode_supports_group(num_q_heads / pool->num_kv_heads))
     return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
   if (!q || !block_table || !seq_lens || !out) return PKV_ERR_INVALID;
@@ -563,7 +617,8 @@ pkv_status pkv_poll_device_error(void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return PKV_ERR_CUDA;
   const uint32_t e = pkv_host::take_append_error(s) | pkv_host::take_decode_error(s) |
                      pkv_host::take_prefill_error(s) | pkv_host::take_qkv_error(s) |
-                     pkv_host::take_multi_error(s);
+                     pkv_host::take_multi_error(s) | pkv_host::take_unpack_error(s) |
+                     pkv_host::take_tables_error(s);
   if (e == ~0u) return PKV_ERR_CUDA;
   if (e & pkv::kErrTimeout) return PKV_ERR_TIMEOUT;
   return e ? PKV_ERR_INVALID : PKV_OK;

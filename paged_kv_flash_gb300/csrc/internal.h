@@ -9,7 +9,7 @@
 namespace pkv_host {
 
 struct AppendLaunch {
-  void* k;                 // pool K (bf16 or int8)
+  void* k;                 // pool K (bf16, int8 or int4 slabs)
   void* v;
   float* k_scale;          // int8 only
   float* v_scale;
@@ -22,11 +22,59 @@ struct AppendLaunch {
   const int32_t* block_table;
   int max_pages;
   const int32_t* seq_lens;
-  const float* k_smooth;   // int8 only, may be null
+  const float* k_smooth;   // int8 and int4, may be null
 };
 
-cudaError_t launch_append(const AppendLaunch& a, bool int8, cudaStream_t s);
+// dtype: the pool's pkv_kv_dtype.
+cudaError_t launch_append(const AppendLaunch& a, int dtype, cudaStream_t s);
 uint32_t take_append_error(cudaStream_t s);
+
+// A quantised pool's positions to bf16 pages (kv_unpack.cu).
+struct UnpackLaunch {
+  const void* k;           // source pool (int8 or int4)
+  const void* v;
+  const float* k_scale;    // int8 only
+  const float* v_scale;
+  int src_pages, num_kv_heads;
+  void* k_out;             // bf16 pool
+  void* v_out;
+  int dst_pages;
+  int batch;
+  const int32_t* src_table;
+  int src_max_pages;
+  const int32_t* dst_table;
+  int dst_max_pages;
+  const int32_t* starts;   // may be null
+  const int32_t* seq_lens;
+  int max_seq_len;
+  const float* k_smooth;   // may be null
+};
+
+cudaError_t launch_unpack(const UnpackLaunch& a, bool int4, cudaStream_t s);
+uint32_t take_unpack_error(cudaStream_t s);
+
+// Block tables and slot maps from request lengths (page_tables.cu).
+struct TablesLaunch {
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int batch;
+  int32_t* ring;
+  int ring_capacity;
+  const int32_t* ring_state;
+  int num_pages;
+  int32_t* table;          // [batch][max_pages]
+  int max_pages;
+  int32_t* seq_lens_out;
+  int32_t* cu_new;         // [batch + 1]
+  int32_t* taken;          // [batch + 1]
+  int32_t* freed;          // [batch + 1]
+  int32_t* slots;          // may be null
+  int slot_capacity;
+  int32_t* ring_state_out;
+};
+
+cudaError_t launch_tables(const TablesLaunch& a, cudaStream_t s);
+uint32_t take_tables_error(cudaStream_t s);
 
 struct DecodeLaunch {
   const void* k;

@@ -9,8 +9,11 @@
 // channels, the max |x| is a warp-shuffle reduction and every step of the
 // quantiser is IEEE fp32 (round-to-nearest division, round-half-even to
 // integer), so the codes and scales are bit-exact against any IEEE fp32
-// implementation of the same steps.
+// implementation of the same steps.  int4: the same steps per group of 32
+// channels (see append_int4_kernel).
 #include <algorithm>
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -121,14 +124,100 @@ __global__ void __launch_bounds__(256) append_int8_kernel(pkv_host::AppendLaunch
   }
 }
 
+// One lane's 8 channels of a vector, whose group is the quad of lanes it lies
+// in: scale and codes of the group.  |x| is compared as an integer (the order
+// of non-negative floats), which keeps a NaN or an infinity at the top: such
+// a group gets a NaN scale.  Returns the codes' word, code + 8 in each nibble.
+__device__ __forceinline__ uint32_t quantize_int4(const float (&x)[8], __half& scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  if (top >= 0x7f800000u) {
+    scale = __ushort_as_half(0x7e00);
+    return 0x88888888u;
+  }
+  scale = __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top), 7.0f), 65504.0f));
+  const float s = __half2float(scale);
+  uint32_t w = 0x88888888u;
+  if (s != 0.0f) {
+    w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = __float2int_rn(__fdiv_rn(x[e], s));    // nearest, ties to even
+      w |= (uint32_t)(max(-7, min(7, c)) + 8) << (4 * e);
+    }
+  }
+  return w;
+}
+
+// Half a warp per (token, head): lane i of 16 holds channels 8i .. 8i + 7 of
+// K and of V (one 16-byte load each), so a group is four lanes and its codes
+// are four 4-byte words of one 16-byte chunk of the slab.  Reads 512 bytes and
+// writes 144 per vector pair.
+__global__ void __launch_bounds__(256) append_int4_kernel(pkv_host::AppendLaunch a) {
+  const int lane = threadIdx.x & 31, i = lane & 15;
+  const long long rows = (long long)a.num_tokens * a.num_kv_heads;
+  const long long nwarps = ((long long)gridDim.x * blockDim.x) >> 5;
+  uint8_t* __restrict__ kp = static_cast<uint8_t*>(a.k);
+  uint8_t* __restrict__ vp = static_cast<uint8_t*>(a.v);
+  const uint4* __restrict__ kn = static_cast<const uint4*>(a.k_new);
+  const uint4* __restrict__ vn = static_cast<const uint4*>(a.v_new);
+  float w[8];
+  if (a.k_smooth) {
+    const float4* ws = reinterpret_cast<const float4*>(a.k_smooth) + 2 * i;
+    const float4 w0 = __ldg(ws), w1 = __ldg(ws + 1);
+    w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w;
+    w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+  }
+  // both halves of a warp run the loop together (the shuffles need them)
+  for (long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; 2 * pair < rows;
+       pair += nwarps) {
+    const long long row = 2 * pair + (lane >> 4);
+    const bool on = row < rows;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 kr = on ? __ldg(kn + row * 16 + i) : none;
+    const uint4 vr = on ? __ldg(vn + row * 16 + i) : none;
+    const long long fs = on ? slot_of_row(a, (int)(row / a.num_kv_heads)) : -1;
+    float x[8] = {bf16lo(kr.x), bf16hi(kr.x), bf16lo(kr.y), bf16hi(kr.y),
+                  bf16lo(kr.z), bf16hi(kr.z), bf16lo(kr.w), bf16hi(kr.w)};
+    if (a.k_smooth) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], w[e]);
+    }
+    __half ks, vs;
+    const uint32_t kc = quantize_int4(x, ks);
+    const float y[8] = {bf16lo(vr.x), bf16hi(vr.x), bf16lo(vr.y), bf16hi(vr.y),
+                        bf16lo(vr.z), bf16hi(vr.z), bf16lo(vr.w), bf16hi(vr.w)};
+    const uint32_t vc = quantize_int4(y, vs);
+    if (fs < 0) continue;
+    const int h = (int)(row % a.num_kv_heads), slot = (int)(fs & 15), g = i >> 2;
+    const size_t slab = ((size_t)(fs >> 4) * a.num_kv_heads + h) * kInt4Slab;
+    const size_t code = slab + g * 256 + slot * 16 + (i & 3) * 4;
+    *reinterpret_cast<uint32_t*>(kp + code) = kc;
+    *reinterpret_cast<uint32_t*>(vp + code) = vc;
+    if ((i & 3) == 0) {
+      const size_t sc = slab + kInt4Codes + slot * 8 + g * 2;
+      *reinterpret_cast<__half*>(kp + sc) = ks;
+      *reinterpret_cast<__half*>(vp + sc) = vs;
+    }
+  }
+}
+
 }  // namespace
 
 namespace pkv_host {
 
-cudaError_t launch_append(const AppendLaunch& a, bool int8, cudaStream_t s) {
+cudaError_t launch_append(const AppendLaunch& a, int dtype, cudaStream_t s) {
   if (a.num_tokens == 0) return cudaSuccess;
   const int sms = sm_count();
-  if (!int8) {
+  if (dtype == PKV_INT4) {
+    const long long warps = ((long long)a.num_tokens * a.num_kv_heads + 1) / 2;
+    const long long blocks = (warps + 7) / 8;
+    const int grid = (int)std::min<long long>(blocks, (long long)sms * 16);
+    append_int4_kernel<<<grid, 256, 0, s>>>(a);
+  } else if (dtype == PKV_BF16) {
     const long long threads = (long long)a.num_tokens * a.num_kv_heads * 16;
     const long long blocks = (threads + 255) / 256;
     const int grid = (int)std::min<long long>(blocks, (long long)sms * 16);

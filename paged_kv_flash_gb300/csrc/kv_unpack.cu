@@ -1,0 +1,132 @@
+// kv_unpack.cu -- the cached positions of a quantised pool (INT4 or INT8)
+// written as bf16 pages, so that the chunked prefill, which reads bf16 pools,
+// can run against a prefix held in fewer bits (TileInfer.jl "Performance" page,
+// "INT8 KV cache": value = code * scale, keys times the smoothing weight).
+//
+// Bound by memory: a (page, KV head) reads 2 x 1,152 bytes (INT4) or 2 x 2,112
+// (INT8) and writes 2 x 4,096.  One warp per (sequence, page, KV head): 16
+// lanes hold a row's 128 channels, 8 each, so every store instruction writes
+// two whole 256-byte rows, and all loads of a slab go out before its stores.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace {
+
+using namespace pkv;
+
+__device__ uint32_t g_err_unpack;
+
+constexpr int kWarps = 8;
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// K or V of one (page, head): this lane's 8 channels of rows 2j + (lane >> 4),
+// j = 0 .. 7, for rows lo <= row < hi.
+template <bool INT4, bool SMOOTH>
+__device__ __forceinline__ void unpack_slab(const void* src, const float* scales, size_t slab,
+                                            uint4* __restrict__ dst, int lo, int hi,
+                                            const float (&w)[8], int lane) {
+  const int i = lane & 15, half = lane >> 4;
+  uint2 code[8];
+  float sc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int row = 2 * j + half;
+    code[j] = make_uint2(0u, 0u);
+    sc[j] = 0.f;
+    if (row < lo || row >= hi) continue;
+    if constexpr (INT4) {
+      const uint8_t* base = static_cast<const uint8_t*>(src) + slab * kInt4Slab;
+      const int g = i >> 2;
+      code[j].x = __ldg(reinterpret_cast<const uint32_t*>(base + g * 256 + row * 16 + (i & 3) * 4));
+      sc[j] = __half2float(__ushort_as_half(__ldg(
+          reinterpret_cast<const unsigned short*>(base + kInt4Codes + row * 8 + g * 2))));
+    } else {
+      const uint8_t* base = static_cast<const uint8_t*>(src) + slab * (kPageSize * kHeadDim);
+      code[j] = __ldg(reinterpret_cast<const uint2*>(base + row * kHeadDim + i * 8));
+      sc[j] = __ldg(scales + slab * kPageSize + row);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int row = 2 * j + half;
+    if (row < lo || row >= hi) continue;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int c;
+      if constexpr (INT4)
+        c = (int)((code[j].x >> (4 * e)) & 15u) - 8;
+      else
+        c = (int)(int8_t)(((e < 4 ? code[j].x : code[j].y) >> (8 * (e & 3))) & 0xffu);
+      x[e] = __fmul_rn((float)c, sc[j]);
+      if constexpr (SMOOTH) x[e] = __fmul_rn(x[e], w[e]);
+    }
+    dst[row * 16 + i] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
+                                   pack2(x[6], x[7]));
+  }
+}
+
+template <bool INT4>
+__global__ void __launch_bounds__(kWarps * 32)
+    unpack_kernel(const __grid_constant__ pkv_host::UnpackLaunch a) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);      // (page, head) of the sequence
+  const int lp = unit / a.num_kv_heads, h = unit % a.num_kv_heads;
+  const int L = __ldg(a.seq_lens + b);
+  const int start = a.starts ? __ldg(a.starts + b) : 0;
+  if (L < 0 || L > a.max_seq_len || start < 0) {
+    if (unit == 0 && lane == 0) atomicOr(&g_err_unpack, kErrBadIndex);
+    return;
+  }
+  const int lo = start - lp * kPageSize, hi = min(kPageSize, L - lp * kPageSize);
+  if (hi <= 0 || lo >= hi) return;
+  const int ps = __ldg(a.src_table + (size_t)b * a.src_max_pages + lp);
+  const int pd = __ldg(a.dst_table + (size_t)b * a.dst_max_pages + lp);
+  if (ps < 0 || ps >= a.src_pages || pd < 0 || pd >= a.dst_pages) {
+    if (lane == 0) atomicOr(&g_err_unpack, kErrBadIndex);
+    return;
+  }
+  const size_t slab = (size_t)ps * a.num_kv_heads + h;
+  const size_t out = ((size_t)pd * a.num_kv_heads + h) * kPageSize * (kHeadDim / 8);   // 16-byte units
+  float w[8];
+  if (a.k_smooth) {
+    const float4* ws = reinterpret_cast<const float4*>(a.k_smooth) + 2 * (lane & 15);
+    const float4 w0 = __ldg(ws), w1 = __ldg(ws + 1);
+    w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w;
+    w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+    unpack_slab<INT4, true>(a.k, a.k_scale, slab, static_cast<uint4*>(a.k_out) + out, lo, hi, w,
+                            lane);
+  } else {
+    unpack_slab<INT4, false>(a.k, a.k_scale, slab, static_cast<uint4*>(a.k_out) + out, lo, hi, w,
+                             lane);
+  }
+  unpack_slab<INT4, false>(a.v, a.v_scale, slab, static_cast<uint4*>(a.v_out) + out, lo, hi, w,
+                           lane);
+}
+
+}  // namespace
+
+namespace pkv_host {
+
+cudaError_t launch_unpack(const UnpackLaunch& a, bool int4, cudaStream_t s) {
+  const long long units =
+      (long long)((a.max_seq_len + kPageSize - 1) / kPageSize) * a.num_kv_heads;
+  const long long blocks = (units + kWarps - 1) / kWarps;
+  const dim3 grid((unsigned)blocks, a.batch);
+  if (int4)
+    unpack_kernel<true><<<grid, kWarps * 32, 0, s>>>(a);
+  else
+    unpack_kernel<false><<<grid, kWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+uint32_t take_unpack_error(cudaStream_t s) { return take_error_word(&g_err_unpack, s); }
+
+}  // namespace pkv_host

@@ -19,8 +19,9 @@ import torch
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpagedkv.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT = 0, -1, -2, -3, -4
-BF16, INT8 = 0, 1
+BF16, INT8, INT4 = 0, 1, 4
 HEAD_DIM, PAGE_SIZE = 128, 16
+INT4_SLAB = 1152                # bytes of one (page, KV head) slab of an INT4 pool
 
 
 class PkvError(RuntimeError):
@@ -43,6 +44,8 @@ _P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size
 _POOLP = ctypes.POINTER(_Pool)
 SIGNATURES = {
     "pkv_kv_append": (_I, [_POOLP, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P]),
+    "pkv_kv_unpack": (_I, [_POOLP, _POOLP, _I, _P, _I, _P, _I, _P, _P, _I, _P, _P]),
+    "pkv_page_tables": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _I, _P, _P]),
     "pkv_decode_plan": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I),
                              ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
     "pkv_paged_attn_decode": (_I, [_POOLP, _P, _I, _I, _P, _I, _P, _I, _F, _P, _I, _P, _SZ,
@@ -107,10 +110,21 @@ def _need(t: torch.Tensor, dtype, name: str):
                          f"{t.dtype} on {t.device} (contiguous={t.is_contiguous()})")
 
 
+def _one_device(what: str, *tensors):
+    """The tensors of one call lie on the current device, where the kernels run
+    (a pointer of another device would fault there)."""
+    now = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != now:
+            raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{now}")
+
+
 @dataclass
 class Pool:
     """A paged KV pool: k, v [num_pages][Hkv][16][128] (bf16 or int8) and, for
-    int8, fp32 scales [num_pages][Hkv][16]."""
+    int8, fp32 scales [num_pages][Hkv][16].  A 4-bit pool (INT4) has uint8 k, v
+    [num_pages][Hkv][1152], codes and scales of a (page, head) together (the
+    slab layout is stated beside pkv_pool)."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: Optional[torch.Tensor] = None
@@ -118,7 +132,7 @@ class Pool:
 
     @property
     def dtype(self) -> int:
-        return INT8 if self.k.dtype == torch.int8 else BF16
+        return {torch.int8: INT8, torch.uint8: INT4}.get(self.k.dtype, BF16)
 
     @property
     def num_pages(self) -> int:
@@ -139,16 +153,26 @@ class Pool:
         cached = self.__dict__.get("_c")
         if cached is None or cached[0] != key:
             self._validate()
-            cached = (key, _Pool(key[0], key[1], key[2], key[3], *key[4], key[7]))
+            cached = (key, _Pool(key[0], key[1], key[2], key[3], *key[4][:2], PAGE_SIZE, HEAD_DIM,
+                                 key[7]))
             self.__dict__["_c"] = cached
         return cached[1]
 
     def _validate(self):
         """The kernels take the pool's pointers as they are: host memory or a
         wrong layout must be refused here, before any launch."""
-        want = torch.int8 if self.k.dtype == torch.int8 else torch.bfloat16
+        want = {INT8: torch.int8, INT4: torch.uint8, BF16: torch.bfloat16}[self.dtype]
         _need(self.k, want, "pool.k")
         _need(self.v, want, "pool.v")
+        if want == torch.uint8:
+            if (self.k.dim() != 3 or self.k.shape[2] != INT4_SLAB
+                    or self.v.shape != self.k.shape or self.v.device != self.k.device):
+                raise ValueError(f"pool: k and v of a 4-bit pool must be [num_pages][Hkv]"
+                                 f"[{INT4_SLAB}] on one device, got {tuple(self.k.shape)} on "
+                                 f"{self.k.device} and {tuple(self.v.shape)} on {self.v.device}")
+            if self.k_scale is not None or self.v_scale is not None:
+                raise ValueError("a 4-bit pool keeps its scales in its slabs")
+            return
         if (self.k.dim() != 4 or tuple(self.k.shape[2:]) != (PAGE_SIZE, HEAD_DIM)
                 or self.v.shape != self.k.shape or self.v.device != self.k.device):
             raise ValueError(f"pool: k and v must be [num_pages][Hkv][{PAGE_SIZE}][{HEAD_DIM}] "
@@ -168,6 +192,10 @@ class Pool:
 
     @staticmethod
     def empty(num_pages: int, num_kv_heads: int, dtype=torch.bfloat16, device="cuda"):
+        """dtype: torch.bfloat16, torch.int8, or torch.uint8 for a 4-bit pool."""
+        if dtype == torch.uint8:
+            return Pool(*(torch.empty((num_pages, num_kv_heads, INT4_SLAB), dtype=torch.uint8,
+                                      device=device) for _ in range(2)))
         shape = (num_pages, num_kv_heads, PAGE_SIZE, HEAD_DIM)
         if dtype == torch.int8:
             return Pool(torch.empty(shape, dtype=torch.int8, device=device),
@@ -193,6 +221,77 @@ def kv_append(pool: Pool, k_new, v_new, cu_new, block_table, seq_lens, k_smooth=
                             block_table.shape[1], _ptr(seq_lens), _ptr(k_smooth),
                             _stream(stream))
     _check(st, "pkv_kv_append")
+
+
+def kv_unpack(src: Pool, dst: Pool, src_block_table, dst_block_table, seq_lens, max_seq_len,
+              starts=None, k_smooth=None, stream=None):
+    """Write positions starts[b] (0 if not given) .. seq_lens[b] - 1 of a 4-bit
+    or INT8 pool into the bf16 pool dst, through a block table of each (see
+    pkv_kv_unpack): what a prefill against a quantised prefix reads."""
+    for t, n in ((src_block_table, "src_block_table"), (dst_block_table, "dst_block_table"),
+                 (seq_lens, "seq_lens")):
+        _need(t, torch.int32, n)
+    B = seq_lens.shape[0]
+    if src_block_table.shape[0] != B or dst_block_table.shape[0] != B:
+        raise ValueError(f"kv_unpack: {B} sequences, but block tables of "
+                         f"{src_block_table.shape[0]} and {dst_block_table.shape[0]} rows")
+    if starts is not None:
+        _need(starts, torch.int32, "starts")
+        if starts.numel() != B:
+            raise ValueError(f"starts: expected {B} entries, got {starts.numel()}")
+    if k_smooth is not None:
+        _need(k_smooth, torch.float32, "k_smooth")
+        if k_smooth.numel() != HEAD_DIM:
+            raise ValueError(f"k_smooth: expected {HEAD_DIM} entries, got {k_smooth.numel()}")
+    sc, dc = src.c(), dst.c()
+    _one_device("kv_unpack", src.k, dst.k, src_block_table, dst_block_table, seq_lens, starts,
+                k_smooth)
+    st = _lib.pkv_kv_unpack(ctypes.byref(sc), ctypes.byref(dc), B, _ptr(src_block_table),
+                            src_block_table.shape[1], _ptr(dst_block_table),
+                            dst_block_table.shape[1], _ptr(starts), _ptr(seq_lens),
+                            int(max_seq_len), _ptr(k_smooth), _stream(stream))
+    _check(st, "pkv_kv_unpack")
+
+
+def page_tables(seq_lens, new_lens, block_table, free_ring, ring_state, num_pages, cu_new=None,
+                page_offsets=None, slot_map=None, seq_lens_out=None, ring_state_out=None,
+                stream=None):
+    """The step's tables from request lengths (see pkv_page_tables): pages of
+    free_ring [capacity] (state int32 [2]: first, count) go to block_table
+    [B][max_pages] for new_lens[b] tokens behind seq_lens[b]; new_lens[b] < 0
+    frees request b's pages.  Without seq_lens_out / ring_state_out the state
+    is updated in place.  All int32.  Returns (cu_new, seq_lens_out)."""
+    B = seq_lens.shape[0]
+    if seq_lens_out is None:
+        seq_lens_out = seq_lens
+    if ring_state_out is None:
+        ring_state_out = ring_state
+    if cu_new is None:
+        cu_new = torch.empty(B + 1, dtype=torch.int32, device=seq_lens.device)
+    if page_offsets is None:
+        page_offsets = torch.empty((2, B + 1), dtype=torch.int32, device=seq_lens.device)
+    for t, n, count in ((seq_lens, "seq_lens", B), (new_lens, "new_lens", B),
+                        (ring_state, "ring_state", 2), (seq_lens_out, "seq_lens_out", B),
+                        (ring_state_out, "ring_state_out", 2), (cu_new, "cu_new", B + 1),
+                        (page_offsets, "page_offsets", 2 * (B + 1)),
+                        (free_ring, "free_ring", None), (block_table, "block_table", None),
+                        (slot_map, "slot_map", None)):
+        if t is None:
+            continue
+        _need(t, torch.int32, n)
+        if count is not None and t.numel() != count:
+            raise ValueError(f"{n}: expected {count} entries, got {t.numel()}")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table: expected [{B}][max_pages], got {tuple(block_table.shape)}")
+    _one_device("page_tables", seq_lens, new_lens, block_table, free_ring, ring_state, cu_new,
+                page_offsets, slot_map, seq_lens_out, ring_state_out)
+    st = _lib.pkv_page_tables(
+        _ptr(seq_lens), _ptr(new_lens), B, _ptr(free_ring), free_ring.numel(), _ptr(ring_state),
+        int(num_pages), _ptr(block_table), block_table.shape[1], _ptr(seq_lens_out),
+        _ptr(cu_new), _ptr(page_offsets), _ptr(slot_map),
+        slot_map.numel() if slot_map is not None else 0, _ptr(ring_state_out), _stream(stream))
+    _check(st, "pkv_page_tables")
+    return cu_new, seq_lens_out
 
 
 def decode_plan(batch, num_q_heads, num_kv_heads, max_seq_len, num_splits=0, dtype=BF16):
