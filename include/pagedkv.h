@@ -121,9 +121,9 @@ pkv_status pkv_kv_append(const pkv_pool* pool, const void* k_new, const void* v_
 /*
  * Split plan of a decode call ("Fused kernels ...": split-KV for decode).
  * Host-only; launches nothing.  max_seq_len (host) bounds every seq_lens[b];
- * dtype is the pool's pkv_kv_dtype (the heuristic plans the two kernels
- * differently: INT8 pages, half the bytes, get longer splits, and the INT8
- * kernel, bound by its work per page, gets a full wave of CTAs); a plan is
+ * dtype is the pool's pkv_kv_dtype (the heuristic plans the kernels
+ * differently: quantised pages, half the bytes or fewer, get longer splits,
+ * and their kernels, bound by their work per page, get a full wave of CTAs); a plan is
  * for its dtype only; num_splits 0 asks for the built-in
  * heuristic (split count chosen from the batch, the heads, the dtype and the
  * device's SM count), > 0 forces that many splits.
@@ -150,8 +150,10 @@ pkv_status pkv_decode_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_he
  *  q            bf16 [batch][num_q_heads][128].
  *  block_table  int32 [batch][max_pages]; seq_lens int32 [batch] (device);
  *               max_seq_len (host) >= every seq_lens[b].
- *  k_smooth     INT8 pools: the same fp32 [128] weight given to kv_append,
- *               or NULL if the keys were not smoothed; NULL for bf16.
+ *  k_smooth     INT8 and INT4 pools: the same fp32 [128] weight given to
+ *               kv_append, or NULL if the keys were not smoothed; NULL for
+ *               bf16.  INT4 pools: q and k_smooth 16-byte aligned, any number
+ *               of query heads per KV head (other pools: 1, 2, 4 or 8).
  *  num_splits   0 = heuristic, > 0 forces (see pkv_decode_plan).
  *  workspace    scratch of at least pkv_decode_plan's bytes for this pool's
  *               dtype and these sizes (256-byte
@@ -340,7 +342,8 @@ pkv_status pkv_decode_multi_plan(int32_t batch, int32_t total_q, int32_t num_q_h
  *             workspace of its size when splits > 1, else may be NULL).
  *  out        bf16 [total_q][num_q_heads][128]; lse fp32 [total_q][Hq]
  *             (natural log) or NULL.
- * bf16 pools only (PKV_ERR_UNSUPPORTED for INT8 and for max_q_len > 16).
+ * bf16 pools only (PKV_ERR_UNSUPPORTED for others -- INT4 pools have
+ * pkv_paged_attn_decode_multi_int4 -- and for max_q_len > 16).
  * A sequence with q_b > max_q_len, seq_lens[b] < q_b, a length past the
  * block table or a page id outside the pool is skipped and flagged for
  * pkv_poll_device_error.
@@ -353,6 +356,22 @@ pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int3
                                        int32_t num_splits, void* workspace,
                                        size_t workspace_bytes, void* out, float* lse,
                                        void* stream);
+
+/*
+ * paged_attn_decode_multi_int4 -- the same on a PKV_INT4 pool
+ * (PKV_ERR_UNSUPPORTED for others).  Plan, workspace and arguments as
+ * pkv_paged_attn_decode_multi's; k_smooth: the fp32 [128] weight given to
+ * kv_append (16-byte aligned), or NULL.
+ */
+pkv_status pkv_paged_attn_decode_multi_int4(const pkv_pool* pool, const void* q, int32_t total_q,
+                                            const int32_t* cu_q, int32_t batch,
+                                            int32_t num_q_heads, const int32_t* block_table,
+                                            int32_t max_pages, const int32_t* seq_lens,
+                                            int32_t max_q_len, int32_t max_seq_len,
+                                            float softmax_scale, const float* k_smooth,
+                                            int32_t num_splits, void* workspace,
+                                            size_t workspace_bytes, void* out, float* lse,
+                                            void* stream);
 
 /*
  * qkv_norm_rope_append -- the fused attention-input step: from the fused

@@ -107,9 +107,9 @@ struct Plan {
   size_t ws_bytes, ws_zero_bytes, ws_o_offset, ws_lse_offset;
 };
 
-// int8: the pool's dtype (longer splits, a full wave of CTAs).
+// quant: an INT8 or INT4 pool (longer splits, a full wave of CTAs).
 Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, int num_splits,
-               bool int8) {
+               bool quant) {
   const int mp = std::max(1, (max_seq_len + pkv::kPageSize - 1) / pkv::kPageSize);
   int C;
   if (num_splits > 0) {
@@ -118,10 +118,10 @@ Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, in
     const long long slots = (long long)sm_count() * pkv_host::kDecodeCtasPerSm;
     const long long page_heads = (long long)batch * num_kv_heads * mp;
     const long long target =
-        std::max<long long>(1, int8 ? slots : slots * kPlanSlotsNum / kPlanSlotsDen);
+        std::max<long long>(1, quant ? slots : slots * kPlanSlotsNum / kPlanSlotsDen);
     long long c = (page_heads + target - 1) / target;
     c = std::max<long long>(kPlanMinPages,
-                            std::min<long long>(int8 ? kPlanMaxPages : kPlanMaxPagesBf16, c));
+                            std::min<long long>(quant ? kPlanMaxPages : kPlanMaxPagesBf16, c));
     c = (c + pkv_host::kDecodeWarps - 1) / pkv_host::kDecodeWarps * pkv_host::kDecodeWarps;
     C = (int)std::min<long long>(c, mp);
   }
@@ -141,6 +141,14 @@ Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, in
     p.ws_bytes = p.ws_lse_offset + (rows * sizeof(float) + 255) / 256 * 256;
   }
   return p;
+}
+
+// What the int4 kernel asks of a call: 16-byte loads of queries and weights,
+// and one CTA per 32 query rows of a KV head in the grid's y.
+pkv_status check_int4(const void* q, const float* k_smooth, int num_kv_heads, int rows) {
+  if (!aligned(q, 16) || (k_smooth && !aligned(k_smooth, 16))) return PKV_ERR_INVALID;
+  if ((long long)num_kv_heads * ((rows + 31) / 32) > 65535) return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
 }
 
 pkv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
@@ -244,11 +252,12 @@ pkv_status pkv_decode_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_he
                            int32_t* splits_out, int32_t* pages_per_split_out,
                            size_t* workspace_bytes_out, size_t* zero_bytes_out) {
   if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
-      max_seq_len < 0 || num_splits < 0 || (dtype != PKV_BF16 && dtype != PKV_INT8))
+      max_seq_len < 0 || num_splits < 0 ||
+      (dtype != PKV_BF16 && dtype != PKV_INT8 && dtype != PKV_INT4))
     return PKV_ERR_INVALID;
   if (num_splits > 1 && (long long)batch * num_kv_heads > kDecodeCounters) return PKV_ERR_INVALID;
   const Plan p = make_plan(batch, num_q_heads, num_kv_heads, max_seq_len, num_splits,
-                           dtype == PKV_INT8);
+                           dtype != PKV_BF16);
   if (splits_out) *splits_out = p.splits;
   if (pages_per_split_out) *pages_per_split_out = p.pages_per_split;
   if (workspace_bytes_out) *workspace_bytes_out = p.ws_bytes;
@@ -321,16 +330,21 @@ static pkv_status decode_call(const pkv_pool* pool, const void* q, int32_t batch
       max_seq_len < 0 || (long long)max_seq_len > (long long)max_pages * pkv::kPageSize ||
       num_splits < 0 || !std::isfinite(softmax_scale))
     return PKV_ERR_INVALID;
-  if (pool->dtype == PKV_INT4 ||
+  if (pool->dtype != PKV_INT4 &&
       !pkv_host::decode_supports_group(num_q_heads / pool->num_kv_heads))
     return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
   if (!q || !block_table || !seq_lens || !out) return PKV_ERR_INVALID;
+  if (pool->dtype == PKV_INT4) {
+    const pkv_status s4 = check_int4(q, k_smooth, pool->num_kv_heads,
+                                     num_q_heads / pool->num_kv_heads);
+    if (s4 != PKV_OK) return s4;
+  }
   if (pool->dtype == PKV_BF16 && k_smooth) return PKV_ERR_INVALID;
   if (num_splits > 1 && (long long)batch * pool->num_kv_heads > kDecodeCounters)
     return PKV_ERR_INVALID;
   const Plan p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, num_splits,
-                           pool->dtype == PKV_INT8);
+                           pool->dtype != PKV_BF16);
   if (p.ws_bytes > 0 && (!workspace || workspace_bytes < p.ws_bytes || !aligned(workspace, 256)))
     return PKV_ERR_INVALID;
   if ((long long)batch > 65535 || p.splits > 2147483647 / 2) return PKV_ERR_UNSUPPORTED;
@@ -354,8 +368,7 @@ static pkv_status decode_call(const pkv_pool* pool, const void* q, int32_t batch
   set_workspace(a, p, workspace, fused);
   a.out = out;
   a.lse = lse;
-  return cuda_status(pkv_host::launch_decode(a, pool->dtype == PKV_INT8,
-                                             static_cast<cudaStream_t>(stream)));
+  return cuda_status(pkv_host::launch_decode(a, pool->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_paged_attn_decode(const pkv_pool* pool, const void* q, int32_t batch,
@@ -395,23 +408,28 @@ pkv_status pkv_paged_attn_decode_noalloc(const pkv_pool* pool, const void* q, in
       max_seq_len < 0 || (long long)max_seq_len > (long long)max_pages * pkv::kPageSize ||
       num_splits < 0 || !std::isfinite(softmax_scale))
     return PKV_ERR_INVALID;
-  if (pool->dtype == PKV_INT4 ||
+  if (pool->dtype != PKV_INT4 &&
       !pkv_host::decode_supports_group(num_q_heads / pool->num_kv_heads))
     return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
   if (!q || !block_table || !seq_lens || !out) return PKV_ERR_INVALID;
+  if (pool->dtype == PKV_INT4) {
+    const pkv_status s4 = check_int4(q, k_smooth, pool->num_kv_heads,
+                                     num_q_heads / pool->num_kv_heads);
+    if (s4 != PKV_OK) return s4;
+  }
   if (pool->dtype == PKV_BF16 && k_smooth) return PKV_ERR_INVALID;
   if (num_splits > 1 && (long long)batch * pool->num_kv_heads > kDecodeCounters)
     return PKV_ERR_INVALID;
   const size_t cap = pkv_host::decode_fixed_scratch_bytes();
-  const bool int8 = pool->dtype == PKV_INT8;
-  Plan p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, num_splits, int8);
+  const bool quant = pool->dtype != PKV_BF16;
+  Plan p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, num_splits, quant);
   if (p.ws_bytes > cap) {
     if (num_splits > 0) return PKV_ERR_INVALID;       // forced split count does not fit
     int s = p.splits;
     while (s > 1 && p.ws_bytes > cap) {
       --s;
-      p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, s, int8);
+      p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, s, quant);
     }
     if (p.ws_bytes > cap) return PKV_ERR_INVALID;
   }
@@ -439,8 +457,7 @@ pkv_status pkv_paged_attn_decode_noalloc(const pkv_pool* pool, const void* q, in
   set_workspace(a, p, scratch, false);
   a.out = out;
   a.lse = lse;
-  return cuda_status(pkv_host::launch_decode(a, pool->dtype == PKV_INT8,
-                                             static_cast<cudaStream_t>(stream)));
+  return cuda_status(pkv_host::launch_decode(a, pool->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_prefill_plan(int32_t* ctas, size_t* workspace_bytes, size_t* zero_bytes) {
@@ -553,14 +570,13 @@ pkv_status pkv_decode_multi_plan(int32_t batch, int32_t total_q, int32_t num_q_h
   return PKV_OK;
 }
 
-pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int32_t total_q,
-                                       const int32_t* cu_q, int32_t batch, int32_t num_q_heads,
-                                       const int32_t* block_table, int32_t max_pages,
-                                       const int32_t* seq_lens, int32_t max_q_len,
-                                       int32_t max_seq_len, float softmax_scale,
-                                       int32_t num_splits, void* workspace,
-                                       size_t workspace_bytes, void* out, float* lse,
-                                       void* stream) {
+static pkv_status multi_call(const pkv_pool* pool, int32_t dtype, const void* q, int32_t total_q,
+                             const int32_t* cu_q, int32_t batch, int32_t num_q_heads,
+                             const int32_t* block_table, int32_t max_pages,
+                             const int32_t* seq_lens, int32_t max_q_len, int32_t max_seq_len,
+                             float softmax_scale, const float* k_smooth, int32_t num_splits,
+                             void* workspace, size_t workspace_bytes, void* out, float* lse,
+                             void* stream) {
   pkv_status st = check_pool(pool);
   if (st != PKV_OK) return st;
   if (batch < 0 || total_q < 0 || num_q_heads <= 0 || num_q_heads % pool->num_kv_heads ||
@@ -568,10 +584,16 @@ pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int3
       (long long)max_seq_len > (long long)max_pages * pkv::kPageSize || num_splits < 0 ||
       !std::isfinite(softmax_scale))
     return PKV_ERR_INVALID;
-  if (pool->dtype != PKV_BF16 || max_q_len > kMultiMaxQ) return PKV_ERR_UNSUPPORTED;
+  if (pool->dtype != dtype || max_q_len > kMultiMaxQ) return PKV_ERR_UNSUPPORTED;
   if (batch == 0 || total_q == 0) return PKV_OK;
   if (!q || !cu_q || !block_table || !seq_lens || !out) return PKV_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(out, 16)) return PKV_ERR_INVALID;
+  const bool int4 = dtype == PKV_INT4;
+  if (int4) {
+    st = check_int4(q, k_smooth, pool->num_kv_heads,
+                    max_q_len * (num_q_heads / pool->num_kv_heads));
+    if (st != PKV_OK) return st;
+  }
   const MultiPlan m = make_multi_plan(batch, total_q, num_q_heads, pool->num_kv_heads, max_q_len,
                                       max_seq_len, num_splits);
   if (m.p.ws_bytes > 0 &&
@@ -595,6 +617,7 @@ pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int3
   a.seq_lens = seq_lens;
   a.max_q = max_q_len;
   a.softmax_scale = softmax_scale;
+  a.k_smooth = k_smooth;
   a.splits = m.p.splits;
   a.pages_per_split = m.p.pages_per_split;
   a.row_groups = m.row_groups;
@@ -603,7 +626,34 @@ pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int3
   a.ws_lse = m.p.ws_bytes ? reinterpret_cast<float*>(base + m.p.ws_lse_offset) : nullptr;
   a.out = out;
   a.lse = lse;
-  return cuda_status(pkv_host::launch_decode_multi(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(pkv_host::launch_decode_multi(a, int4, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int32_t total_q,
+                                       const int32_t* cu_q, int32_t batch, int32_t num_q_heads,
+                                       const int32_t* block_table, int32_t max_pages,
+                                       const int32_t* seq_lens, int32_t max_q_len,
+                                       int32_t max_seq_len, float softmax_scale,
+                                       int32_t num_splits, void* workspace,
+                                       size_t workspace_bytes, void* out, float* lse,
+                                       void* stream) {
+  return multi_call(pool, PKV_BF16, q, total_q, cu_q, batch, num_q_heads, block_table, max_pages,
+                    seq_lens, max_q_len, max_seq_len, softmax_scale, nullptr, num_splits,
+                    workspace, workspace_bytes, out, lse, stream);
+}
+
+pkv_status pkv_paged_attn_decode_multi_int4(const pkv_pool* pool, const void* q, int32_t total_q,
+                                            const int32_t* cu_q, int32_t batch,
+                                            int32_t num_q_heads, const int32_t* block_table,
+                                            int32_t max_pages, const int32_t* seq_lens,
+                                            int32_t max_q_len, int32_t max_seq_len,
+                                            float softmax_scale, const float* k_smooth,
+                                            int32_t num_splits, void* workspace,
+                                            size_t workspace_bytes, void* out, float* lse,
+                                            void* stream) {
+  return multi_call(pool, PKV_INT4, q, total_q, cu_q, batch, num_q_heads, block_table, max_pages,
+                    seq_lens, max_q_len, max_seq_len, softmax_scale, k_smooth, num_splits,
+                    workspace, workspace_bytes, out, lse, stream);
 }
 
 pkv_status pkv_selftest_bounded_wait(const uint32_t* counter, uint32_t target, void* stream) {
@@ -618,7 +668,7 @@ pkv_status pkv_poll_device_error(void* stream) {
   const uint32_t e = pkv_host::take_append_error(s) | pkv_host::take_decode_error(s) |
                      pkv_host::take_prefill_error(s) | pkv_host::take_qkv_error(s) |
                      pkv_host::take_multi_error(s) | pkv_host::take_unpack_error(s) |
-                     pkv_host::take_tables_error(s);
+                     pkv_host::take_tables_error(s) | pkv_host::take_int4_error(s);
   if (e == ~0u) return PKV_ERR_CUDA;
   if (e & pkv::kErrTimeout) return PKV_ERR_TIMEOUT;
   return e ? PKV_ERR_INVALID : PKV_OK;

@@ -939,9 +939,11 @@ namespace pkv_host {
 
 bool decode_supports_group(int g) { return g == 1 || g == 2 || g == 4 || g == 8; }
 
-cudaError_t launch_decode(const DecodeLaunch& a, bool int8, cudaStream_t s) {
+cudaError_t launch_decode(const DecodeLaunch& a, int dtype, cudaStream_t s) {
   if (a.batch == 0) return cudaSuccess;
-  cudaError_t e = int8 ? dispatch_i8mma(a, s) : dispatch_group(a, s);
+  cudaError_t e = dtype == PKV_INT4   ? launch_split_int4(a, s)
+                  : dtype == PKV_INT8 ? dispatch_i8mma(a, s)
+                                      : dispatch_group(a, s);
   if (e != cudaSuccess || a.splits == 1 || a.ws_ctr) return e;
   // the combine's CTAs are placed while the split kernel's last ones run and
   // wait on the device for its partials, instead of a launch after it

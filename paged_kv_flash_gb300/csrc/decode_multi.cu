@@ -452,8 +452,7 @@ __global__ void __launch_bounds__(128)
 
 namespace pkv_host {
 
-cudaError_t launch_decode_multi(const MultiLaunch& a, cudaStream_t s) {
-  if (a.batch == 0 || a.total_q == 0) return cudaSuccess;
+static cudaError_t launch_multi_bf16(const MultiLaunch& a, cudaStream_t s) {
   cudaError_t e = pkv_host::set_max_dynamic_smem(
       reinterpret_cast<const void*>(decode_multi_kernel), SMEM);
   if (e != cudaSuccess) return e;
@@ -465,7 +464,12 @@ cudaError_t launch_decode_multi(const MultiLaunch& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   dim3 grid(a.splits, a.num_kv_heads * a.row_groups, a.batch);
   decode_multi_kernel<<<grid, kThreads, SMEM, s>>>(tk, tv, a);
-  e = cudaGetLastError();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decode_multi(const MultiLaunch& a, bool int4, cudaStream_t s) {
+  if (a.batch == 0 || a.total_q == 0) return cudaSuccess;
+  const cudaError_t e = int4 ? launch_multi_int4(a, s) : launch_multi_bf16(a, s);
   if (e != cudaSuccess || a.splits == 1) return e;
   // placed while the split kernel's last CTAs run; waits for its partials
   return pkv_host::launch_dependent(decode_multi_combine_kernel, dim3(a.total_q * a.num_q_heads),

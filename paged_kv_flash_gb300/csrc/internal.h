@@ -109,7 +109,8 @@ constexpr int kDecodeCtasPerSm = 2;      // split CTAs per SM the plan counts on
 bool encode_int8_slab_map(void* map, const void* base, int num_pages, int hkv);
 
 bool decode_supports_group(int group);
-cudaError_t launch_decode(const DecodeLaunch& a, bool int8, cudaStream_t s);
+// dtype: the pool's pkv_kv_dtype.
+cudaError_t launch_decode(const DecodeLaunch& a, int dtype, cudaStream_t s);
 uint32_t take_decode_error(cudaStream_t s);
 
 // Fixed device scratch for pkv_paged_attn_decode_noalloc (decode.cu).
@@ -120,7 +121,7 @@ cudaError_t decode_fixed_scratch(void** ptr);
 
 // Split-KV decode of 1..16 query tokens per sequence (decode_multi.cu).
 struct MultiLaunch {
-  const void* k;           // bf16 pool
+  const void* k;           // bf16 or int4 pool
   const void* v;
   int num_pages, num_kv_heads;
   const void* q;           // bf16 [total_q][Hq][128]
@@ -132,16 +133,23 @@ struct MultiLaunch {
   const int32_t* seq_lens; // [B], the step's tokens included
   int max_q;               // tokens per sequence at most (<= 16)
   float softmax_scale;
+  const float* k_smooth;   // int4 pool only, may be null
   int splits, pages_per_split;
-  int row_groups;          // ceil(max_q * G / 64): CTAs per (split, KV head, sequence)
+  int row_groups;          // ceil(max_q * G / 64): CTAs per (split, KV head, sequence), bf16
   float* ws_o;             // [total_q * Hq][splits][128] when splits > 1
   float* ws_lse;           // [total_q * Hq][splits]
   void* out;               // bf16 [total_q][Hq][128]
   float* lse;              // [total_q][Hq] or null
 };
 
-cudaError_t launch_decode_multi(const MultiLaunch& a, cudaStream_t s);
+cudaError_t launch_decode_multi(const MultiLaunch& a, bool int4, cudaStream_t s);
 uint32_t take_multi_error(cudaStream_t s);
+
+// The split kernel of both on an int4 pool (decode_int4.cu); launch_decode and
+// launch_decode_multi add the combine.  workspace as theirs.
+cudaError_t launch_split_int4(const DecodeLaunch& a, cudaStream_t s);
+cudaError_t launch_multi_int4(const MultiLaunch& a, cudaStream_t s);
+uint32_t take_int4_error(cudaStream_t s);
 // cuTensorMapEncodeTiled of a bf16 pool (K or V) as 2-D rows of 128
 // channels, one box per 16-row x 64-channel half slab, 128B-swizzled
 // (prefill.cu); `map` points to a CUtensorMap.

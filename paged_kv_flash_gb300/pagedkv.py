@@ -62,6 +62,8 @@ SIGNATURES = {
                                    ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
     "pkv_paged_attn_decode_multi": (_I, [_POOLP, _P, _I, _P, _I, _I, _P, _I, _P, _I, _I, _F, _I,
                                          _P, _SZ, _P, _P, _P]),
+    "pkv_paged_attn_decode_multi_int4": (_I, [_POOLP, _P, _I, _P, _I, _I, _P, _I, _P, _I, _I, _F,
+                                              _P, _I, _P, _SZ, _P, _P, _P]),
     "pkv_qkv_norm_rope_append": (_I, [_POOLP, _P, _I, _I, _P, _P, _F, _P, _P, _I, _P, _I, _P,
                                       _I, _P, _P, _P]),
     "pkv_selftest_bounded_wait": (_I, [_P, ctypes.c_uint32, _P]),
@@ -108,6 +110,12 @@ def _need(t: torch.Tensor, dtype, name: str):
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor, got "
                          f"{t.dtype} on {t.device} (contiguous={t.is_contiguous()})")
+
+
+def _need_smooth(k_smooth: torch.Tensor):
+    _need(k_smooth, torch.float32, "k_smooth")
+    if k_smooth.numel() != HEAD_DIM:
+        raise ValueError(f"k_smooth: expected {HEAD_DIM} entries, got {k_smooth.numel()}")
 
 
 def _one_device(what: str, *tensors):
@@ -240,9 +248,7 @@ def kv_unpack(src: Pool, dst: Pool, src_block_table, dst_block_table, seq_lens, 
         if starts.numel() != B:
             raise ValueError(f"starts: expected {B} entries, got {starts.numel()}")
     if k_smooth is not None:
-        _need(k_smooth, torch.float32, "k_smooth")
-        if k_smooth.numel() != HEAD_DIM:
-            raise ValueError(f"k_smooth: expected {HEAD_DIM} entries, got {k_smooth.numel()}")
+        _need_smooth(k_smooth)
     sc, dc = src.c(), dst.c()
     _one_device("kv_unpack", src.k, dst.k, src_block_table, dst_block_table, seq_lens, starts,
                 k_smooth)
@@ -296,7 +302,7 @@ def page_tables(seq_lens, new_lens, block_table, free_ring, ring_state, num_page
 
 def decode_plan(batch, num_q_heads, num_kv_heads, max_seq_len, num_splits=0, dtype=BF16):
     """(splits, pages_per_split, workspace_bytes, zero_bytes) of a decode call
-    on a pool of the given dtype (BF16 or INT8)."""
+    on a pool of the given dtype (BF16, INT8 or INT4)."""
     s, c, w, z = _I(), _I(), _SZ(), _SZ()
     st = _lib.pkv_decode_plan(batch, num_q_heads, num_kv_heads, max_seq_len, int(dtype),
                               num_splits, ctypes.byref(s), ctypes.byref(c), ctypes.byref(w),
@@ -436,17 +442,18 @@ def decode_multi_plan(batch, total_q, num_q_heads, num_kv_heads, max_q_len, max_
 
 def paged_attn_decode_multi(pool: Pool, q, cu_q, block_table, seq_lens, max_q_len, max_seq_len,
                             softmax_scale, num_splits=0, workspace=None, out=None, lse=None,
-                            want_lse=True, stream=None):
+                            want_lse=True, stream=None, k_smooth=None):
     """1..16 query tokens per sequence, causal inside the step (verify steps):
-    q [total_q][Hq][128] bf16 -> (out bf16, lse fp32).  The workspace is
-    allocated when not given."""
+    q [total_q][Hq][128] bf16 -> (out bf16, lse fp32), on a bf16 or a 4-bit
+    pool (k_smooth: 4-bit pools only).  The workspace is allocated when not
+    given."""
     _need(q, torch.bfloat16, "q")
     for t, n in ((cu_q, "cu_q"), (block_table, "block_table"), (seq_lens, "seq_lens")):
         _need(t, torch.int32, n)
     T, Hq, _ = q.shape
     B = seq_lens.shape[0]
     if workspace is None:
-        _, _, wsb = decode_multi_plan(B, T, Hq, pool.k.shape[1], int(max_q_len),
+        _, _, wsb = decode_multi_plan(B, T, Hq, pool.num_kv_heads, int(max_q_len),
                                       int(max_seq_len), num_splits)
         workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=q.device)
     if out is None:
@@ -454,12 +461,19 @@ def paged_attn_decode_multi(pool: Pool, q, cu_q, block_table, seq_lens, max_q_le
     if lse is None and want_lse:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     pc = pool.c()
-    st = _lib.pkv_paged_attn_decode_multi(
+    if k_smooth is not None:
+        if pool.dtype != INT4:
+            raise ValueError("k_smooth: the verify steps of 4-bit pools alone take it")
+        _need_smooth(k_smooth)
+    int4 = pool.dtype == INT4
+    fn = _lib.pkv_paged_attn_decode_multi_int4 if int4 else _lib.pkv_paged_attn_decode_multi
+    st = fn(
         ctypes.byref(pc), _ptr(q), T, _ptr(cu_q), B, Hq, _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), int(max_q_len), int(max_seq_len), float(softmax_scale), int(num_splits),
+        _ptr(seq_lens), int(max_q_len), int(max_seq_len), float(softmax_scale),
+        *((_ptr(k_smooth),) if int4 else ()), int(num_splits),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
         _stream(stream))
-    _check(st, "pkv_paged_attn_decode_multi")
+    _check(st, "pkv_paged_attn_decode_multi_int4" if int4 else "pkv_paged_attn_decode_multi")
     return out, lse
 
 

@@ -72,11 +72,11 @@ def fill(rng, layout, lens, Hkv, w=None, poison=0xFF):
 
 def attention(k_pool, v_pool, q, cu_q, block_table, seq_lens, scale, w=None):
     """Causal attention (bottom-right aligned) of q float [T][Hq][128] in
-    float64: (out [T][Hq][128], natural-log lse [T][Hq])."""
+    float64: (out [T][Hq][128], natural-log lse [T][Hq], sum p |v| [T][Hq][128])."""
     T, Hq, _ = q.shape
     Hkv = k_pool.shape[1]
     G = Hq // Hkv
-    out, lse = np.zeros((T, Hq, 128)), np.full((T, Hq), -np.inf)
+    out, lse, mag = np.zeros((T, Hq, 128)), np.full((T, Hq), -np.inf), np.zeros((T, Hq, 128))
     for b, L in enumerate(np.asarray(seq_lens)):
         L, t0, t1 = int(L), int(cu_q[b]), int(cu_q[b + 1])
         if L == 0 or t1 == t0:
@@ -94,5 +94,6 @@ def attention(k_pool, v_pool, q, cu_q, block_table, seq_lens, scale, w=None):
             p = np.exp(s - m)
             l = p.sum(-1, keepdims=True)
             out[t] = (np.einsum("hgn,hnd->hgd", p, v[:, :n]) / l).reshape(Hq, 128)
+            mag[t] = (np.einsum("hgn,hnd->hgd", p, np.abs(v[:, :n])) / l).reshape(Hq, 128)
             lse[t] = (m + np.log(l)).reshape(Hq)
-    return out, lse
+    return out, lse, mag

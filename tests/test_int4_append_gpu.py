@@ -250,7 +250,7 @@ def test_chunked_prefill_against_a_4bit_prefix(pk, smooth):
                                     np.array([T], np.int32), 128 ** -0.5)
     check_out(torch.cat(outs), ro, "chunked prefill")
     check_lse(torch.cat(lses), rl, "chunked prefill")
-    fo, _ = R.attention(pool.k.cpu().numpy(), pool.v.cpu().numpy(),
+    fo, _, _ = R.attention(pool.k.cpu().numpy(), pool.v.cpu().numpy(),
                         W.bits_to_float(q).astype(np.float64), [0, T], layout.block_table, [T],
                         128 ** -0.5, w)
     # bf16 pages: a score is off by at most eps = 2^-9 scale sum|q k|, so every p and the sum of

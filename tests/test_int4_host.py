@@ -144,3 +144,63 @@ def test_page_tables_binding_checks_sizes(monkeypatch):
                 dict(seq_lens_out=i(4)), dict(ring_state_out=i(1))):
         with pytest.raises(ValueError):
             pk.page_tables(**{**good, **bad})
+
+
+# ------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("bad", [dict(Hq=3), dict(q=None), dict(out=None), dict(B=-1),
+                                 dict(max_seq_len=65), dict(scale=float("nan")), dict(splits=-2),
+                                 dict(q=FAKE + 8), dict(smooth=FAKE + 4)])
+def test_int4_decode_refuses_bad_arguments(lib, bad):  # noqa: F811
+    assert decode(lib, int4_pool(), **bad) == INVALID
+
+
+def test_int4_decode_takes_any_group_and_checks_its_workspace(lib):  # noqa: F811
+    assert decode(lib, int4_pool(), B=0, Hq=6) == 0
+    assert decode(lib, int4_pool(), Hq=6, splits=4) == INVALID           # no workspace
+    assert decode(lib, int4_pool(num_kv_heads=65536), Hq=65536) == UNSUPPORTED
+    s, c, w, z = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.pkv_decode_plan(1, 12, 2, 64, 4, 4, ctypes.byref(s), ctypes.byref(c),
+                               ctypes.byref(w), ctypes.byref(z)) == 0
+    assert (s.value, c.value, z.value) == (4, 1, 65536 * 4)
+    assert decode(lib, int4_pool(), Hq=12, splits=4, ws=FAKE, ws_bytes=w.value - 1) == INVALID
+
+
+def multi(lib, name, pool, **kw):  # noqa: F811
+    a = dict(q=FAKE, T=4, cu=FAKE, B=2, Hq=4, bt=FAKE, mp=4, sl=FAKE, mq=2, L=64, scale=0.1,
+             smooth=None, splits=1, ws=None, wsb=0, out=FAKE)
+    a.update(kw)
+    f = getattr(lib, name)
+    f.restype = ctypes.c_int32
+    smooth = [V(a["smooth"])] if name.endswith("int4") else []
+    return f(ctypes.byref(pool), V(a["q"]), a["T"], V(a["cu"]), a["B"], a["Hq"], V(a["bt"]), a["mp"],
+             V(a["sl"]), a["mq"], a["L"], ctypes.c_float(a["scale"]), *smooth, a["splits"],
+             V(a["ws"]), ctypes.c_size_t(a["wsb"]), V(a["out"]), None, None)
+
+
+@pytest.mark.parametrize("bad", [dict(Hq=3), dict(q=FAKE + 4), dict(out=FAKE + 4), dict(mq=0),
+                                 dict(L=65), dict(splits=2), dict(smooth=FAKE + 8), dict(cu=None),
+                                 dict(scale=float("inf"))])
+def test_int4_verify_refuses_bad_arguments(lib, bad):  # noqa: F811
+    assert multi(lib, "pkv_paged_attn_decode_multi_int4", int4_pool(), **bad) == INVALID
+
+
+def test_int4_verify_is_for_4bit_pools(lib):  # noqa: F811
+    name = "pkv_paged_attn_decode_multi_int4"
+    assert multi(lib, name, good_pool()) == UNSUPPORTED
+    assert multi(lib, "pkv_paged_attn_decode_multi", int4_pool()) == UNSUPPORTED
+    assert multi(lib, name, int4_pool(), mq=17) == UNSUPPORTED
+    assert multi(lib, name, int4_pool(num_kv_heads=40000), Hq=80000 * 16, mq=16) == UNSUPPORTED
+    assert multi(lib, name, int4_pool(), T=0) == 0
+
+
+def test_verify_binding_refuses_weights_for_bf16_pools(monkeypatch):
+    monkeypatch.setattr(pk, "_need", lambda *a: None)
+    monkeypatch.setattr(pk, "_stream", lambda s: None)
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    pool = pk.Pool.empty(4, 2, device="cpu")
+    with pytest.raises(ValueError, match="k_smooth"):
+        pk.paged_attn_decode_multi(pool, q, i, i.view(1, 2), i[:1], 1, 16, 0.1, workspace=ws,
+                                   k_smooth=torch.ones(128))
