@@ -34,6 +34,8 @@
 // f16 reaches from 2^-24 to 65504, so p is taken against the running maximum
 // of score + log2(the key's largest V scale, rounded up to a power of two):
 // P' <= 2^15 for any V, and the sum of p stays in fp32.
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -50,13 +52,19 @@ constexpr int kPageBytes = 2 * kInt4Slab;           // K slab, then V slab
 constexpr float kNoKey = -1.0e30f;                  // running max before any visible key
 constexpr float kShift = 7.f;                       // p carries 2^7: P' <= 2^(8 + 7)
 
-// Page buffers per warp: at least what the parked results of 8 NT rows need.
-constexpr int bufs_of(int nt) { return nt == 1 ? 4 : (8 * nt * (kHeadDim + 2) * 4 + kPageBytes - 1) / kPageBytes; }
+// Pages that a warp takes at a time: two where the registers allow (the wait,
+// the maximum's shuffles and votes are per step), and buffers per warp: at
+// least what the parked results of 8 NT rows need.
+constexpr int pages_of_step(int nt) { return nt <= 2 ? 2 : 1; }
+constexpr int bufs_of(int nt) {
+  return nt <= 2 ? 2 : (8 * nt * (kHeadDim + 2) * 4 + kPageBytes - 1) / kPageBytes;
+}
 // The query fragments of all n-tiles wait in shared memory when there are
 // several (NT x 8 k-steps x 32 lanes x 8 bytes, twice with a low part).
 constexpr int qfrag_bytes(int nt, bool smooth) { return nt == 1 ? 0 : nt * 2048 * (smooth ? 2 : 1); }
+constexpr int warp_bytes(int nt) { return bufs_of(nt) * pages_of_step(nt) * kPageBytes; }
 constexpr int smem_of(int nt, bool smooth) {
-  return 1024 + qfrag_bytes(nt, smooth) + W * bufs_of(nt) * kPageBytes;
+  return 1024 + qfrag_bytes(nt, smooth) + W * warp_bytes(nt);
 }
 
 struct Launch {
@@ -88,16 +96,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// D = A B + (c0, c1) in both row halves.
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1, float c0,
-                                             float c1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %11, %10, %11};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -114,25 +112,26 @@ __device__ __forceinline__ float2 halves(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// Upper bound of log2 of the largest of a key's four V scales (fp16, >= 0),
-// from the exponent field E: scale < 2^(E - 14).
-__device__ __forceinline__ float scale_exponent(uint2 s) {
-  const uint32_t m = __vmaxu2(s.x, s.y);
-  const uint32_t e = max(m & 0xffffu, m >> 16) >> 10;
-  return __uint_as_float(0x4B000000u | e) - (8388608.f + 14.f);
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&x),
+                            *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
 }
 
 // This lane's part of query row q0 (128 channels; null: zeros) as B fragments
 // of the 8 k-steps: hi[2 g + s] = channels (0, 4) + 2s and (1, 5) + 2s of the
 // lane's eight channels 32 g + 8 qd .. of group g, the latter divided by 16,
-// all times the power of two that puts the row's largest magnitude into
-// [2^13, 2^14).  With SMOOTH the channels are multiplied by the key weight and
-// lo holds what f16 leaves of them (hi + lo is good to 2^-22).  Without it a
-// bf16 query is exact in f16 down to 2^-30 of the row's maximum.  Returns the
-// power of two that undoes the scaling.
+// all times `sign` and the power of two that puts the row's largest magnitude
+// into [2^13, 2^14).  With SMOOTH the channels are multiplied by the key weight
+// and lo holds what f16 leaves of them (hi + lo is good to 2^-22).  Without it a
+// bf16 query is exact in f16 down to 2^-30 of the row's maximum.  off: the B
+// fragment of -8 sum(q) of the four groups, f16 high parts in rows 0-3 and low
+// parts in rows 4-7 (good to 2^-22).  Returns the power of two that undoes the
+// scaling.
 template <bool SMOOTH>
-__device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const float* w, int qd,
-                                             uint32_t (&hi)[8][2], uint32_t (&lo)[SMOOTH ? 8 : 1][2]) {
+__device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const float* w, float sign,
+                                             int qd, uint32_t (&hi)[8][2],
+                                             uint32_t (&lo)[SMOOTH ? 8 : 1][2], uint32_t& off) {
   float x[4][8];
   float top = 0.f;
 #pragma unroll
@@ -158,9 +157,11 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
   // 2^(13 - floor(log2 top)), within 2^+-100
   const int sh = max(-100, min(100, 13 + 127 - (__float_as_int(top) >> 23)));
-  const float f = __int_as_float((127 + sh) << 23);
+  const float f = sign * __int_as_float((127 + sh) << 23);
+  float sum[4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
+  for (int g = 0; g < 4; ++g) {
+    sum[g] = 0.f;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -168,12 +169,25 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
         const float fj = j ? f * 0.0625f : f;
         const float y0 = x[g][2 * s + j] * fj, y1 = x[g][2 * s + j + 4] * fj;
         const uint32_t h2 = pack_f16x2(y0, y1);
+        const float2 h = halves(h2);
+        float both = h.x + h.y;
         hi[2 * g + s][j] = h2;
         if constexpr (SMOOTH) {
-          const float2 h = halves(h2);
-          lo[2 * g + s][j] = pack_f16x2(y0 - h.x, y1 - h.y);
+          const uint32_t l2 = pack_f16x2(y0 - h.x, y1 - h.y);
+          const float2 l = halves(l2);
+          lo[2 * g + s][j] = l2;
+          both += l.x + l.y;
         }
+        sum[g] += j ? 16.f * both : both;
       }
+    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+    sum[g] *= -8.f / 16777216.f;
+  }
+  const float c0 = (qd & 1) ? sum[2] : sum[0], c1 = (qd & 1) ? sum[3] : sum[1];
+  const uint32_t ch = pack_f16x2(c0, c1);
+  const float2 cf = halves(ch);
+  off = qd < 2 ? ch : pack_f16x2(c0 - cf.x, c1 - cf.y);
   return __int_as_float((127 - sh) << 23);
 }
 
@@ -181,13 +195,14 @@ template <int NT, bool SMOOTH>
 __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     decode_int4_kernel(const __grid_constant__ Launch a) {
   constexpr uint32_t FULL = 0xffffffffu;
-  constexpr int NB = bufs_of(NT);
+  constexpr int NB = bufs_of(NT), NP = pages_of_step(NT);
   constexpr uint32_t NIB0 = 0x000F000Fu, NIB1 = 0x00F000F0u;
   pdl_trigger();                                    // the combine may be placed now
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
   uint8_t* bufs = smem + 1024 + qfrag_bytes(NT, SMOOTH);
   static_assert(W * NB * 8 <= 1016, "barriers fit the header");
+  static_assert(8 * NT * (kHeadDim + 2) * 4 <= warp_bytes(NT), "a warp's results fit its ring");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, qd = lane & 3;
@@ -195,12 +210,14 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   const int h = blockIdx.y / a.row_groups, rg = blockIdx.y % a.row_groups;
   const int Hq = a.num_q_heads, G = a.group;
 
-  // the length, this warp's first 32 page ids and the rows' offsets go out first
+  // The length, this warp's first 32 page ids and the rows' offsets go out
+  // first.  Step j of the warp is pages p_begin + NP (warp + j W) + 0 .. NP - 1;
+  // lane l of an id word holds page l % NP of step l / NP.
   const int32_t* bt_row = a.block_table + (size_t)b * a.max_pages;
   const int p_begin = split * a.pages_per_split;
+  auto id_page = [&](int j) { return p_begin + NP * (warp + (j + lane / NP) * W) + lane % NP; };
   int L = a.seq_lens[b];
-  const int lp0 = p_begin + warp + lane * W;
-  const int bt_first = lp0 < a.max_pages ? __ldg(bt_row + lp0) : 0;
+  const int bt_first = id_page(0) < a.max_pages ? __ldg(bt_row + id_page(0)) : 0;
   int q0 = b, qn = 1;
   if (a.cu_q) {
     q0 = a.cu_q[b];
@@ -210,21 +227,27 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
         atomicOr(&g_err_int4, kErrBadIndex);
       return;
     }
+    if (qn == 0) return;                            // no token in this step
   } else if (L < 0 || L > a.max_pages * kPageSize) {
     if (threadIdx.x == 0) atomicOr(&g_err_int4, kErrBadIndex);
     L = 0;
   }
-  const int R = qn * G, row0 = rg * 8 * NT;         // rows of (b, h); the CTA's first
+  // the rows of (b, h), their n-tiles shared evenly by as many CTAs as need be
+  const int R = qn * G, tiles = (R + 7) >> 3;
+  const int per = NT == 1 ? 1 : (tiles + (tiles + NT - 1) / NT - 1) / max(1, (tiles + NT - 1) / NT);
+  const int row0 = rg * 8 * per;
   if (row0 >= R) return;
+  const int nt_used = NT == 1 ? 1 : min(per, tiles - rg * per);
   const int npages = (L + kPageSize - 1) / kPageSize;
   if (split > 0 && p_begin >= npages) return;       // empty split: the merge skips it
   const int nv = max(1, (npages + a.pages_per_split - 1) / a.pages_per_split);
   const bool direct = a.splits == 1 || nv == 1;
   const int p_end = min(npages, p_begin + a.pages_per_split);
-  const int n_w = max(0, (p_end - p_begin - warp + W - 1) / W);   // pages of this warp
+  const int L_end = min(L, p_end * kPageSize);      // a step may reach past the split
+  const int n_w = max(0, (p_end - p_begin - NP * warp + NP * W - 1) / (NP * W));   // steps
 
   const uint32_t bar0 = smem_u32(bars + warp * NB);
-  uint8_t* wbuf = bufs + (size_t)warp * NB * kPageBytes;
+  uint8_t* wbuf = bufs + (size_t)warp * warp_bytes(NT);
   const uint32_t wbuf_s = smem_u32(wbuf);
   if (lane == 0) {
 #pragma unroll
@@ -234,51 +257,64 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   __syncwarp();
 
   const uint64_t policy = l2_policy_evict_first();
-  int bt_cache = 0;
-  auto page_id = [&](int i) -> int {                // ids of this warp's pages, 32 at a time
-    if ((i & 31) == 0) {
-      const int lp = p_begin + warp + (i + lane) * W;
-      bt_cache = (i + lane < n_w) ? (i == 0 ? bt_first : __ldg(bt_row + lp)) : 0;
+  int ids = 0;
+  auto checked = [&](int id, int page) {            // 0 for what is not to be read
+    if (page >= p_end) return 0;
+    if (id < 0 || id >= a.num_pages) {
+      atomicOr(&g_err_int4, kErrBadIndex);
+      return 0;
     }
-    int pg = __shfl_sync(FULL, bt_cache, i & 31);
-    if (pg < 0 || pg >= a.num_pages) {
-      if (lane == 0) atomicOr(&g_err_int4, kErrBadIndex);
-      pg = 0;
-    }
-    return pg;
+    return id;
   };
-  auto issue = [&](int i, int pg) {
+  const uint8_t* k_head = a.k + (size_t)h * kInt4Slab;
+  const uint8_t* v_head = a.v + (size_t)h * kInt4Slab;
+  const size_t page_stride = (size_t)a.num_kv_heads * kInt4Slab;
+  auto issue = [&](int j) {
+    constexpr int kSteps = 32 / NP;                 // steps of an id word
+    if (j % kSteps == 0) {
+      const int pg = id_page(j);
+      ids = checked(j == 0 ? bt_first : (pg < p_end ? __ldg(bt_row + pg) : 0), pg);
+    }
+    int id[NP];
+#pragma unroll
+    for (int u = 0; u < NP; ++u) id[u] = __shfl_sync(FULL, ids, (j % kSteps) * NP + u);
     if (lane == 0) {
-      const int k = i % NB;
-      const uint32_t bar = bar0 + 8 * k, dst = wbuf_s + k * kPageBytes;
-      const size_t at = ((size_t)pg * a.num_kv_heads + h) * kInt4Slab;
+      const int k = j % NB;
+      const uint32_t bar = bar0 + 8 * k, dst = wbuf_s + k * (NP * kPageBytes);
+      const int n = min(NP, p_end - (p_begin + NP * (warp + j * W)));
       // the warp's reads of this buffer are done (__syncwarp); order them
       // before the async-proxy refill
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive_expect_tx(bar, kPageBytes);
-      bulk_g2s_hint(dst, a.k + at, kInt4Slab, bar, policy);
-      bulk_g2s_hint(dst + kInt4Slab, a.v + at, kInt4Slab, bar, policy);
+      mbar_arrive_expect_tx(bar, n * kPageBytes);
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        if (u >= n) break;
+        bulk_g2s_hint(dst + u * kPageBytes, k_head + id[u] * page_stride, kInt4Slab, bar, policy);
+        bulk_g2s_hint(dst + u * kPageBytes + kInt4Slab, v_head + id[u] * page_stride, kInt4Slab,
+                      bar, policy);
+      }
     }
   };
   const int pro = min(NB, n_w);
-  for (int i = 0; i < pro; ++i) issue(i, page_id(i));
+  for (int j = 0; j < pro; ++j) issue(j);
   int issued = pro;
 
   // Query fragments (column r of n-tile nt = row row0 + 8 nt + r) and, for
   // this lane's accumulator columns 2 qd + e, the factor from raw scores to
-  // the log2 domain and the last position the row sees.
-  uint32_t qh[NT == 1 ? 8 : 1][2], ql[NT == 1 && SMOOTH ? 8 : 1][2];
+  // the log2 domain (never negative: the scale's sign is in the query) and the
+  // last position the row sees.
+  uint32_t qh[NT == 1 ? 8 : 1][2], ql[NT == 1 && SMOOTH ? 8 : 1][2], off[NT];
   uint2* qs = reinterpret_cast<uint2*>(smem + 1024);      // [hi | lo][nt][k-step][lane]
   float sl2[NT][2];
   int lim[NT][2];
-  auto row_ptr = [&](int n) -> const __nv_bfloat16* {     // null for padding rows
-    const int rho = row0 + n;
-    return rho < R ? a.q + ((size_t)(q0 + rho / G) * Hq + h * G + rho % G) * kHeadDim : nullptr;
-  };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     uint32_t hi[8][2], lo[SMOOTH ? 8 : 1][2];
-    const float back = query_frags<SMOOTH>(row_ptr(8 * nt + r), a.k_smooth, qd, hi, lo);
+    const int rq = row0 + 8 * nt + r;
+    const __nv_bfloat16* q =
+        rq < R ? a.q + ((size_t)(q0 + rq / G) * Hq + h * G + rq % G) * kHeadDim : nullptr;
+    const float back =
+        query_frags<SMOOTH>(q, a.k_smooth, a.softmax_scale < 0.f ? -1.f : 1.f, qd, hi, lo, off[nt]);
     if constexpr (NT == 1) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
@@ -301,16 +337,16 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     for (int e = 0; e < 2; ++e) {
       const int rho = row0 + 8 * nt + 2 * qd + e;
       // raw scores are in units of 2^-24
-      sl2[nt][e] = a.softmax_scale * kLog2e * 16777216.f * __shfl_sync(FULL, back, (2 * qd + e) * 4);
-      lim[nt][e] = rho < R ? L - qn + rho / G : L - 1;
+      sl2[nt][e] = fabsf(a.softmax_scale) * (kLog2e * 16777216.f) *
+                   __shfl_sync(FULL, back, (2 * qd + e) * 4);
+      lim[nt][e] = min(L_end - 1, rho < R ? L - qn + rho / G : L - 1);
     }
   }
   if constexpr (NT > 1) __syncthreads();
-  int lim_min = L - 1;                              // pages up to it need no mask
+  int lim_min = L_end - 1;                          // steps up to it need no mask
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) lim_min = min(lim_min, min(lim[nt][0], lim[nt][1]));
-#pragma unroll
-  for (int x = 16; x >= 1; x >>= 1) lim_min = min(lim_min, __shfl_xor_sync(FULL, lim_min, x));
+  lim_min = __reduce_min_sync(FULL, lim_min);
 
   auto q_frag = [&](int nt, int ks, bool low) -> uint2 {
     if constexpr (NT == 1) {
@@ -322,31 +358,15 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       return qs[(((low ? NT : 0) + nt) * 8 + ks) * 32 + lane];
     }
   };
-  // -8 sum(q) of each group, by the MMA itself: A = -8 in every code
-  float c0[NT][4], c1[NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint2 f = q_frag(nt, 2 * g + s, false);
-        mma_f16(d, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, f.x, f.y);
-        if constexpr (SMOOTH) {
-          const uint2 fl = q_frag(nt, 2 * g + s, true);
-          mma_f16(d, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, fl.x, fl.y);
-        }
-      }
-      c0[nt][g] = d[0];
-      c1[nt][g] = d[1];
-    }
 
   // O^T of n-tile nt, group g, half t: channels 32 g + 4 r + 2 t (o[..][0..1])
   // and + 1 (o[..][2..3], times 16) of columns 2 qd, 2 qd + 1, in units of
-  // 2^-24 and with the codes' offset of 8; cs: 8 sum(P') of group r / 2
+  // 2^-24 and with the codes' offset of 8; cs: 8 sum(P') of group r / 2.
+  // mu: the maximum the exponentials are taken against; p carries 2^(kShift -
+  // vexp), where every V scale so far is below 2^vexp.
   float o[NT][8][4], cs[NT][4];
   float mu[NT][2], l[NT][2];
+  int vexp = 0;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -358,163 +378,212 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     mu[nt][0] = mu[nt][1] = kNoKey;
     l[nt][0] = l[nt][1] = 0.f;
   }
-
-  bool failed = false;
-  int i_fail = 0;
-  for (int i = 0; i < n_w; ++i) {
-    const int k = i % NB;
-    if (!__all_sync(FULL, mbar_wait(bar0 + 8 * k, (uint32_t)(i / NB) & 1u))) {
-      failed = true;
-      i_fail = i;
-      break;
+  auto rescale = [&](int nt, float a0, float a1) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      o[nt][q][0] *= a0;
+      o[nt][q][2] *= a0;
+      o[nt][q][1] *= a1;
+      o[nt][q][3] *= a1;
     }
-    const int key0 = (p_begin + warp + i * W) * kPageSize;
-    const bool masked = key0 + kPageSize - 1 > lim_min;           // warp-uniform
-    const uint32_t kst = wbuf_s + k * kPageBytes, vst = kst + kInt4Slab;
-    const uint8_t* kb = wbuf + k * kPageBytes;
+    cs[nt][0] *= a0;
+    cs[nt][1] *= a1;
+    l[nt][0] *= a0;
+    l[nt][1] *= a1;
+  };
 
-    // scales of keys r and r + 8
-    const uint2 ks0 = *reinterpret_cast<const uint2*>(kb + kInt4Codes + r * 8);
-    const uint2 ks1 = *reinterpret_cast<const uint2*>(kb + kInt4Codes + r * 8 + 64);
-    uint2 vs0 = *reinterpret_cast<const uint2*>(kb + kInt4Slab + kInt4Codes + r * 8);
-    uint2 vs1 = *reinterpret_cast<const uint2*>(kb + kInt4Slab + kInt4Codes + r * 8 + 64);
-    if (masked) {                    // slots past the sequence may hold anything
-      if (key0 + r >= L) vs0 = make_uint2(0u, 0u);
-      if (key0 + r + 8 >= L) vs1 = make_uint2(0u, 0u);
+  // One step: the NP pages in the buffer at kb, whose first key is key0.
+  // MASKED: it holds the causal edge or the end of the sequence or the split.
+  auto step = [&](const uint8_t* kb, uint32_t kst, int key0, auto masked_tag) {
+    constexpr bool MASKED = decltype(masked_tag)::value;
+    // V scales of keys 2 qd, 2 qd + 1 (a) and + 8 (b): words (g0 g1, g2 g3) of
+    // each; slots past the sequence may hold anything
+    uint4 va[NP], vb[NP];
+    uint32_t vm = 0;
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const uint8_t* sc = kb + u * kPageBytes + kInt4Slab + kInt4Codes;
+      va[u] = *reinterpret_cast<const uint4*>(sc + qd * 16);
+      vb[u] = *reinterpret_cast<const uint4*>(sc + 64 + qd * 16);
+      if constexpr (MASKED) {
+        const int left = L_end - (key0 + u * kPageSize + 2 * qd);     // valid from this lane's first key on
+        if (left <= 0) va[u].x = va[u].y = 0u;
+        if (left <= 1) va[u].z = va[u].w = 0u;
+        if (left <= 8) vb[u].x = vb[u].y = 0u;
+        if (left <= 9) vb[u].z = vb[u].w = 0u;
+      }
+      vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(va[u].x, va[u].y), __vmaxu2(va[u].z, va[u].w)));
+      vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(vb[u].x, vb[u].y), __vmaxu2(vb[u].z, vb[u].w)));
+    }
+    // a scale of 2^vexp or more (its fp16 exponent field E: scale < 2^(E - 14))
+    const int ve = (int)(max(vm & 0xffffu, vm >> 16) >> 10) - 14;
+    if (__any_sync(FULL, ve > vexp)) {
+      const int now = __reduce_max_sync(FULL, ve);
+      const float f = __int_as_float((127 + vexp - now) << 23);
+      vexp = now;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) rescale(nt, f, f);
     }
 
-    float s[NT][4];
+    // raw scores s = sum_g scale (sum u q - 8 sum q) of keys r and r + 8
+    float s[NP][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < NP; ++u) {
+      const uint8_t* kc = kb + u * kPageBytes;
+      const uint32_t kcs = kst + u * kPageBytes;
+      const uint2 ks0 = *reinterpret_cast<const uint2*>(kc + kInt4Codes + r * 8);
+      const uint2 ks1 = *reinterpret_cast<const uint2*>(kc + kInt4Codes + r * 8 + 64);
+      const uint32_t t0 = (qd & 1) ? ks0.y : ks0.x, t1 = (qd & 1) ? ks1.y : ks1.x;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+        mma_f16(s[u][nt], t0, t1, 0u, 0u, off[nt], 0u);
+      }
 #pragma unroll
-    for (int g2 = 0; g2 < 2; ++g2) {
-      uint32_t kw[4];                // group 2 g2: keys r, r + 8; group 2 g2 + 1: the same
-      ldsm_x4(kst + g2 * 512 + lane * 16, kw);
+      for (int g2 = 0; g2 < 2; ++g2) {
+        uint32_t kw[4];              // group 2 g2: keys r, r + 8; group 2 g2 + 1: the same
+        ldsm_x4(kcs + g2 * 512 + lane * 16, kw);
+        const float2 fa = halves(g2 ? ks0.y : ks0.x), fb = halves(g2 ? ks1.y : ks1.x);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int g = 2 * g2 + u;
-        const uint32_t w0 = kw[2 * u], w1 = kw[2 * u + 1];
-        const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
-        const uint32_t sa = g < 2 ? ks0.x : ks0.y, sb = g < 2 ? ks1.x : ks1.y;
-        const float f0 = (g & 1) ? halves(sa).y : halves(sa).x;
-        const float f1 = (g & 1) ? halves(sb).y : halves(sb).x;
+        for (int w = 0; w < 2; ++w) {
+          const int g = 2 * g2 + w;
+          const uint32_t w0 = kw[2 * w], w1 = kw[2 * w + 1];
+          const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
+          const float f0 = w ? fa.y : fa.x, f1 = w ? fb.y : fb.x;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float d[4];
-          const uint2 fa = q_frag(nt, 2 * g, false), fb = q_frag(nt, 2 * g + 1, false);
-          mma_f16_from(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, fa.x, fa.y, c0[nt][g],
-                       c1[nt][g]);
-          mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, fb.x, fb.y);
-          if constexpr (SMOOTH) {
-            const uint2 la = q_frag(nt, 2 * g, true), lb = q_frag(nt, 2 * g + 1, true);
-            mma_f16(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, la.x, la.y);
-            mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, lb.x, lb.y);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (NT > 1 && nt >= nt_used) break;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint2 qa = q_frag(nt, 2 * g, false), qb = q_frag(nt, 2 * g + 1, false);
+            mma_f16(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, qa.x, qa.y);
+            mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, qb.x, qb.y);
+            if constexpr (SMOOTH) {
+              const uint2 la = q_frag(nt, 2 * g, true), lb = q_frag(nt, 2 * g + 1, true);
+              mma_f16(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, la.x, la.y);
+              mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, lb.x, lb.y);
+            }
+            s[u][nt][0] = fmaf(f0, d[0], s[u][nt][0]);
+            s[u][nt][1] = fmaf(f0, d[1], s[u][nt][1]);
+            s[u][nt][2] = fmaf(f1, d[2], s[u][nt][2]);
+            s[u][nt][3] = fmaf(f1, d[3], s[u][nt][3]);
           }
-          s[nt][0] = fmaf(f0, d[0], s[nt][0]);
-          s[nt][1] = fmaf(f0, d[1], s[nt][1]);
-          s[nt][2] = fmaf(f1, d[2], s[nt][2]);
-          s[nt][3] = fmaf(f1, d[3], s[nt][3]);
         }
       }
     }
 
-    // softmax: the running max (of score + the key's V exponent) moves only
-    // when a page passes it by more than 8
-    const float e0 = scale_exponent(vs0), e1 = scale_exponent(vs1);
-    float p[NT][4];
+    // softmax; P of a page as the B fragment's two words (keys 2 qd, 2 qd + 1
+    // and + 8 of head r), in f16
+    uint32_t pw[NP][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      bool on[4] = {true, true, true, true};
-      float t[4];
+      if (NT > 1 && nt >= nt_used) break;
+      auto sees = [&](int u, int j) {
+        return key0 + u * kPageSize + r + (j < 2 ? 0 : 8) <= lim[nt][j & 1];
+      };
+      float pm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = fmaf(s[nt][j], sl2[nt][j & 1], j < 2 ? e0 : e1);
-      if (masked) {
+      for (int u = 0; u < NP; ++u)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          on[j] = key0 + r + (j < 2 ? 0 : 8) <= lim[nt][j & 1];
-          if (!on[j]) t[j] = -INFINITY;
+          if constexpr (MASKED) {
+            if (sees(u, j)) pm[j & 1] = fmaxf(pm[j & 1], s[u][nt][j]);
+          } else {
+            pm[j & 1] = fmaxf(pm[j & 1], s[u][nt][j]);
+          }
         }
-      }
-      float pm[2] = {fmaxf(t[0], t[2]), fmaxf(t[1], t[3])};
 #pragma unroll
       for (int x = 4; x <= 16; x <<= 1) {
         pm[0] = fmaxf(pm[0], __shfl_xor_sync(FULL, pm[0], x));
         pm[1] = fmaxf(pm[1], __shfl_xor_sync(FULL, pm[1], x));
       }
-      float alpha[2] = {1.f, 1.f};
-      bool grow = false;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (pm[e] > mu[nt][e] + 8.f) {
-          alpha[e] = fast_exp2(mu[nt][e] - pm[e]);
-          mu[nt][e] = pm[e];
-          l[nt][e] *= alpha[e];
-          grow = true;
-        }
-      if (__any_sync(FULL, grow)) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          o[nt][q][0] *= alpha[0];
-          o[nt][q][2] *= alpha[0];
-          o[nt][q][1] *= alpha[1];
-          o[nt][q][3] *= alpha[1];
-        }
-        cs[nt][0] *= alpha[0];
-        cs[nt][1] *= alpha[1];
+      // the maximum moves only when a step passes it by more than 8
+      pm[0] *= sl2[nt][0];
+      pm[1] *= sl2[nt][1];
+      const bool g0 = pm[0] > mu[nt][0] + 8.f, g1 = pm[1] > mu[nt][1] + 8.f;
+      if (__any_sync(FULL, g0 || g1)) {
+        const float a0 = g0 ? fast_exp2(mu[nt][0] - pm[0]) : 1.f;
+        const float a1 = g1 ? fast_exp2(mu[nt][1] - pm[1]) : 1.f;
+        if (g0) mu[nt][0] = pm[0];
+        if (g1) mu[nt][1] = pm[1];
+        rescale(nt, a0, a1);
       }
-      const float sub0 = kShift - mu[nt][0], sub1 = kShift - mu[nt][1];
+      const float sub0 = kShift - (float)vexp - mu[nt][0], sub1 = kShift - (float)vexp - mu[nt][1];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[nt][j] = fast_exp2(fmaf(s[nt][j], sl2[nt][j & 1], (j & 1) ? sub1 : sub0));
-        if (masked && !on[j]) p[nt][j] = 0.f;
+      for (int u = 0; u < NP; ++u) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[j] = fast_exp2(fmaf(s[u][nt][j], sl2[nt][j & 1], (j & 1) ? sub1 : sub0));
+          if constexpr (MASKED) {
+            if (!sees(u, j)) p[j] = 0.f;
+          }
+        }
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
+        pw[u][nt][0] = movm_t(pack_f16x2(p[0], p[1]));
+        pw[u][nt][1] = movm_t(pack_f16x2(p[2], p[3]));
       }
-      l[nt][0] += p[nt][0] + p[nt][2];
-      l[nt][1] += p[nt][1] + p[nt][3];
     }
 
     // O += V P', group by group
 #pragma unroll
-    for (int g2 = 0; g2 < 2; ++g2) {
-      uint32_t vw[4];
-      ldsm_x4_t(vst + g2 * 512 + lane * 16, vw);
+    for (int u = 0; u < NP; ++u) {
+      const uint32_t vcs = kst + u * kPageBytes + kInt4Slab;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int g = 2 * g2 + u;
-        const uint32_t w0 = vw[2 * u], w1 = vw[2 * u + 1];
-        const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
-        const uint32_t sa = g < 2 ? vs0.x : vs0.y, sb = g < 2 ? vs1.x : vs1.y;
-        const float f0 = (g & 1) ? halves(sa).y : halves(sa).x;
-        const float f1 = (g & 1) ? halves(sb).y : halves(sb).x;
-        const uint32_t eight = (r >> 1) == g ? 0x00080008u : 0u;
+      for (int g2 = 0; g2 < 2; ++g2) {
+        uint32_t vw[4];
+        ldsm_x4_t(vcs + g2 * 512 + lane * 16, vw);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t pb0 = movm_t(pack_f16x2(p[nt][0] * f0, p[nt][1] * f0));
-          const uint32_t pb1 = movm_t(pack_f16x2(p[nt][2] * f1, p[nt][3] * f1));
-          mma_f16(o[nt][2 * g], w0 & NIB0, w0 & NIB1, w1 & NIB0, w1 & NIB1, pb0, pb1);
-          mma_f16(o[nt][2 * g + 1], x0 & NIB0, x0 & NIB1, x1 & NIB0, x1 & NIB1, pb0, pb1);
-          mma_f16(cs[nt], eight, 0u, eight, 0u, pb0, pb1);
+        for (int w = 0; w < 2; ++w) {
+          const int g = 2 * g2 + w;
+          const uint32_t w0 = vw[2 * w], w1 = vw[2 * w + 1];
+          const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
+          const uint32_t sel = w ? 0x7632u : 0x5410u;    // group g of two keys' words
+          const uint32_t sa = __byte_perm(g2 ? va[u].y : va[u].x, g2 ? va[u].w : va[u].z, sel);
+          const uint32_t sb = __byte_perm(g2 ? vb[u].y : vb[u].x, g2 ? vb[u].w : vb[u].z, sel);
+          const uint32_t eight = (r >> 1) == g ? 0x00080008u : 0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (NT > 1 && nt >= nt_used) break;
+            const uint32_t pb0 = mul_f16x2(pw[u][nt][0], sa), pb1 = mul_f16x2(pw[u][nt][1], sb);
+            mma_f16(o[nt][2 * g], w0 & NIB0, w0 & NIB1, w1 & NIB0, w1 & NIB1, pb0, pb1);
+            mma_f16(o[nt][2 * g + 1], x0 & NIB0, x0 & NIB1, x1 & NIB0, x1 & NIB1, pb0, pb1);
+            mma_f16(cs[nt], eight, 0u, eight, 0u, pb0, pb1);
+          }
         }
       }
     }
-    __syncwarp();
-    if (issued < n_w) {
-      issue(issued, page_id(issued));
-      ++issued;
+  };
+
+  bool failed = false;
+  int j_fail = 0;
+  for (int j = 0; j < n_w; ++j) {
+    const int k = j % NB;
+    if (!__all_sync(FULL, mbar_wait(bar0 + 8 * k, (uint32_t)(j / NB) & 1u))) {
+      failed = true;
+      j_fail = j;
+      break;
     }
+    const int key0 = (p_begin + NP * (warp + j * W)) * kPageSize;
+    const int at = k * (NP * kPageBytes);
+    if (key0 + NP * kPageSize - 1 <= lim_min)
+      step(wbuf + at, wbuf_s + at, key0, std::false_type{});
+    else
+      step(wbuf + at, wbuf_s + at, key0, std::true_type{});
+    __syncwarp();
+    if (issued < n_w) issue(issued++);
   }
   if (failed) {
     if (lane == 0) atomicOr(&g_err_int4, kErrTimeout);
     // let every copy this warp issued land (bounded) before the buffers are
     // reused or the CTA exits
-    for (int i = i_fail; i < issued; ++i)
-      (void)mbar_wait(bar0 + 8 * (i % NB), (uint32_t)(i / NB) & 1u);
+    for (int j = j_fail; j < issued; ++j)
+      (void)mbar_wait(bar0 + 8 * (j % NB), (uint32_t)(j / NB) & 1u);
   }
   __syncwarp();
 
   // Park (O unnormalised, m, l) of the warp's rows in its buffers (all of its
-  // copies have landed): O [8 NT][128], m [8 NT], l [8 NT].
+  // copies have landed): O [8 NT][128], m [8 NT], l [8 NT]; m is where p = 1.
   float* wo = reinterpret_cast<float*>(wbuf);
   float* wm = wo + 8 * NT * kHeadDim;
   float* wl = wm + 8 * NT;
@@ -544,7 +613,8 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     if (r == 0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        wm[8 * nt + 2 * qd + e] = failed ? kNoKey : mu[nt][e];
+        const bool none = failed || mu[nt][e] == kNoKey;
+        wm[8 * nt + 2 * qd + e] = none ? kNoKey : mu[nt][e] + (float)vexp;
         wl[8 * nt + 2 * qd + e] = failed ? 0.f : l[nt][e];
       }
     }
@@ -553,8 +623,8 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
 
   // Merge the warps (log-sum-exp rule); write the bf16 output (one split) or
   // the split's partial.
-  constexpr size_t kStride = (size_t)NB * kPageBytes;
-  const int rows = min(8 * NT, R - row0);
+  constexpr size_t kStride = warp_bytes(NT);
+  const int rows = min(8 * nt_used, R - row0);
   for (int t = threadIdx.x; t < rows * kHeadDim; t += W * 32) {
     const int n = t / kHeadDim, d = t % kHeadDim;
     float M = kNoKey;
@@ -594,7 +664,7 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     uint32_t old;
     asm volatile("fence.acq_rel.gpu;\n\tatom.relaxed.gpu.global.add.u32 %0, [%1], 1;"
                  : "=r"(old) : "l"(ctr) : "memory");
-    const bool last = old == (uint32_t)nv * ((R + 8 * NT - 1) / (8 * NT)) - 1u;
+    const bool last = old == (uint32_t)(nv * ((tiles + per - 1) / per)) - 1u;
     if (last) {
       asm volatile("fence.acq_rel.gpu;" ::: "memory");
       *ctr = 0u;
