@@ -144,10 +144,10 @@ Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, in
 }
 
 // What the int4 kernel asks of a call: 16-byte loads of queries and weights,
-// and one CTA per 32 query rows of a KV head in the grid's y.
+// and one CTA per 8 query rows of a KV head in the grid's y.
 pkv_status check_int4(const void* q, const float* k_smooth, int num_kv_heads, int rows) {
   if (!aligned(q, 16) || (k_smooth && !aligned(k_smooth, 16))) return PKV_ERR_INVALID;
-  if ((long long)num_kv_heads * ((rows + 31) / 32) > 65535) return PKV_ERR_UNSUPPORTED;
+  if ((long long)num_kv_heads * (((long long)rows + 7) / 8) > 65535) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
 

@@ -15,9 +15,10 @@
 // What is left of the encoding is put right outside the loop over the page:
 //   2^-20 against 2^-24: the query channels that meet bits 4-7 are divided by
 //     16 beforehand (QK), the output rows afterwards (PV);
-//   the 8 in u = code + 8: QK starts its accumulators at -8 sum(q) of the
-//     group; PV counts sum(P') in one extra MMA per group and takes 8 sum(P')
-//     off at the end.
+//   the 8 in u = code + 8: -8 sum(q) scale of the groups starts the scores (one
+//     MMA a page over the four scales), 8 sum(P') comes off the outputs at the
+//     end (an MMA a group adds it up: of the rounded P', so that a code of 0
+//     gives 0 whatever P' rounds to).
 //
 // One CTA per (split, KV head x row group, sequence), mma.sync m16n8k16, f16
 // in, fp32 out.  A warp takes whole pages of its split, round-robin, from a
@@ -28,12 +29,13 @@
 //     score (fp32);
 //   O^T += V^T P'^T: A = V^T by ldmatrix.trans, whose 16-bit elements are four
 //     channels of one key, so that a register pairs the keys the MMA wants;
-//     B = P' = p * scale of the group, rounded to f16 (half a step is 2^-12 of
-//     the value, against 2^-9 for the bf16 P of the bf16 kernel) and moved to
-//     the B layout by movmatrix.
+//     B = P' = p * scale of the group, p and the product rounded to f16 (2^-11 of
+//     the value each at most, against 2^-8 for the bf16 P of the bf16 kernel), p
+//     moved to the B layout by movmatrix before it is scaled: two scales of two
+//     keys at once.
 // f16 reaches from 2^-24 to 65504, so p is taken against the running maximum
-// of score + log2(the key's largest V scale, rounded up to a power of two):
-// P' <= 2^15 for any V, and the sum of p stays in fp32.
+// and a power of two above the V scales: P' <= 2^15 (see the loop); the sum of p
+// stays in fp32.
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -48,24 +50,31 @@ using namespace pkv;
 __device__ uint32_t g_err_int4;
 
 constexpr int W = 4;                                // warps per CTA
+constexpr int kCtasPerSm = 4;
+constexpr int kRows = 8;                            // query rows of a CTA: one n-tile
+// A warp takes two pages at a time (the wait, the maximum's shuffles and the
+// votes are per step), from a ring of two such buffers; the sixteen warps of an
+// SM then have 74 KB or more in flight.
+constexpr int NP = 2, NB = 2;
 constexpr int kPageBytes = 2 * kInt4Slab;           // K slab, then V slab
+constexpr int kStepBytes = NP * kPageBytes, kStepKeys = NP * kPageSize;
+constexpr int kWarpBytes = NB * kStepBytes;
+static_assert(kRows * (kHeadDim + 2) * 4 <= kWarpBytes, "a warp's results fit its ring");
 constexpr float kNoKey = -1.0e30f;                  // running max before any visible key
-constexpr float kShift = 7.f;                       // p carries 2^7: P' <= 2^(8 + 7)
+constexpr int kShift = 7;                           // p carries 2^7: P' <= 2^(8 + 7)
+constexpr int kMargin = 3;                          // octaves V scales may grow unwatched
+// How a query with key weights (more bits than f16 holds) is given: not at
+// all; a low part in MMAs of its own; or, with at most four rows, in the
+// n-tile's other four columns.
+constexpr int kPlain = 0, kLowApart = 1, kLowBeside = 2;
 
-// Pages that a warp takes at a time: two where the registers allow (the wait,
-// the maximum's shuffles and votes are per step), and buffers per warp: at
-// least what the parked results of 8 NT rows need.
-constexpr int pages_of_step(int nt) { return nt <= 2 ? 2 : 1; }
-constexpr int bufs_of(int nt) {
-  return nt <= 2 ? 2 : (8 * nt * (kHeadDim + 2) * 4 + kPageBytes - 1) / kPageBytes;
-}
-// The query fragments of all n-tiles wait in shared memory when there are
-// several (NT x 8 k-steps x 32 lanes x 8 bytes, twice with a low part).
-constexpr int qfrag_bytes(int nt, bool smooth) { return nt == 1 ? 0 : nt * 2048 * (smooth ? 2 : 1); }
-constexpr int warp_bytes(int nt) { return bufs_of(nt) * pages_of_step(nt) * kPageBytes; }
-constexpr int smem_of(int nt, bool smooth) {
-  return 1024 + qfrag_bytes(nt, smooth) + W * warp_bytes(nt);
-}
+// Shared memory: barriers (256 bytes), the query's offset fragment and scale
+// factors, then its B fragments (8 k-steps x 32 lanes x 8 bytes, twice with a
+// low part: in registers they would cost 16 or 32 of them, a CTA per SM,
+// against 4 or 8 loads a page), then the warps' rings.
+constexpr int qfrag_bytes(int low) { return 2048 * (low == kLowApart ? 2 : 1); }
+constexpr int smem_of(int low) { return 1024 + qfrag_bytes(low) + W * kWarpBytes; }
+static_assert(kCtasPerSm * (smem_of(kLowApart) + 1024) <= 228 * 1024, "resident CTAs");
 
 struct Launch {
   const uint8_t* k;
@@ -96,6 +105,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B.  The zeros come in registers (see kernel): as constants they cost
+// four moves before every such MMA.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1,
+                                            const float (&z)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]),
+        "f"(z[3]));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -104,7 +125,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -122,16 +143,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
 // of the 8 k-steps: hi[2 g + s] = channels (0, 4) + 2s and (1, 5) + 2s of the
 // lane's eight channels 32 g + 8 qd .. of group g, the latter divided by 16,
 // all times `sign` and the power of two that puts the row's largest magnitude
-// into [2^13, 2^14).  With SMOOTH the channels are multiplied by the key weight
+// into [2^13, 2^14).  With key weights the channels are multiplied by the key weight
 // and lo holds what f16 leaves of them (hi + lo is good to 2^-22).  Without it a
 // bf16 query is exact in f16 down to 2^-30 of the row's maximum.  off: the B
 // fragment of -8 sum(q) of the four groups, f16 high parts in rows 0-3 and low
 // parts in rows 4-7 (good to 2^-22).  Returns the power of two that undoes the
 // scaling.
-template <bool SMOOTH>
+template <int LOW>
 __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const float* w, float sign,
                                              int qd, uint32_t (&hi)[8][2],
-                                             uint32_t (&lo)[SMOOTH ? 8 : 1][2], uint32_t& off) {
+                                             uint32_t (&lo)[LOW ? 8 : 1][2], uint32_t& off) {
   float x[4][8];
   float top = 0.f;
 #pragma unroll
@@ -144,7 +165,7 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
       x[g][2 * e] = bf16lo(r4[e]);
       x[g][2 * e + 1] = bf16hi(r4[e]);
     }
-    if constexpr (SMOOTH) {
+    if constexpr (LOW != kPlain) {
       const float4* ws = reinterpret_cast<const float4*>(w + 32 * g + 8 * qd);
       const float4 w0 = __ldg(ws), w1 = __ldg(ws + 1);
       x[g][0] *= w0.x, x[g][1] *= w0.y, x[g][2] *= w0.z, x[g][3] *= w0.w;
@@ -172,7 +193,7 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
         const float2 h = halves(h2);
         float both = h.x + h.y;
         hi[2 * g + s][j] = h2;
-        if constexpr (SMOOTH) {
+        if constexpr (LOW != kPlain) {
           const uint32_t l2 = pack_f16x2(y0 - h.x, y1 - h.y);
           const float2 l = halves(l2);
           lo[2 * g + s][j] = l2;
@@ -191,18 +212,19 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
   return __int_as_float((127 - sh) << 23);
 }
 
-template <int NT, bool SMOOTH>
-__global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
+template <int LOW>
+__global__ void __launch_bounds__(W * 32, kCtasPerSm)
     decode_int4_kernel(const __grid_constant__ Launch a) {
   constexpr uint32_t FULL = 0xffffffffu;
-  constexpr int NB = bufs_of(NT), NP = pages_of_step(NT);
   constexpr uint32_t NIB0 = 0x000F000Fu, NIB1 = 0x00F000F0u;
+  constexpr uint32_t kEight = 0x48004800u;          // (8, 8) in f16
   pdl_trigger();                                    // the combine may be placed now
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
-  uint8_t* bufs = smem + 1024 + qfrag_bytes(NT, SMOOTH);
-  static_assert(W * NB * 8 <= 1016, "barriers fit the header");
-  static_assert(8 * NT * (kHeadDim + 2) * 4 <= warp_bytes(NT), "a warp's results fit its ring");
+  uint32_t* s_off = reinterpret_cast<uint32_t*>(smem + 256);            // [lane]
+  float* s_back = reinterpret_cast<float*>(smem + 384);                 // [row]
+  uint2* qs = reinterpret_cast<uint2*>(smem + 1024);                    // [hi | lo][k-step][lane]
+  uint8_t* bufs = smem + 1024 + qfrag_bytes(LOW);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, qd = lane & 3;
@@ -211,11 +233,12 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   const int Hq = a.num_q_heads, G = a.group;
 
   // The length, this warp's first 32 page ids and the rows' offsets go out
-  // first.  Step j of the warp is pages p_begin + NP (warp + j W) + 0 .. NP - 1;
-  // lane l of an id word holds page l % NP of step l / NP.
+  // first.  Step j of the warp is pages p0 + NP W j + 0 .. NP - 1; lane l of an
+  // id word holds page l % NP of step l / NP.
   const int32_t* bt_row = a.block_table + (size_t)b * a.max_pages;
   const int p_begin = split * a.pages_per_split;
-  auto id_page = [&](int j) { return p_begin + NP * (warp + (j + lane / NP) * W) + lane % NP; };
+  const int p0 = p_begin + NP * warp;
+  auto id_page = [&](int j) { return p0 + NP * W * (j + lane / NP) + lane % NP; };
   int L = a.seq_lens[b];
   const int bt_first = id_page(0) < a.max_pages ? __ldg(bt_row + id_page(0)) : 0;
   int q0 = b, qn = 1;
@@ -227,27 +250,22 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
         atomicOr(&g_err_int4, kErrBadIndex);
       return;
     }
-    if (qn == 0) return;                            // no token in this step
   } else if (L < 0 || L > a.max_pages * kPageSize) {
     if (threadIdx.x == 0) atomicOr(&g_err_int4, kErrBadIndex);
     L = 0;
   }
-  // the rows of (b, h), their n-tiles shared evenly by as many CTAs as need be
-  const int R = qn * G, tiles = (R + 7) >> 3;
-  const int per = NT == 1 ? 1 : (tiles + (tiles + NT - 1) / NT - 1) / max(1, (tiles + NT - 1) / NT);
-  const int row0 = rg * 8 * per;
+  const int R = qn * G, row0 = rg * kRows;          // rows of (b, h); the CTA's first
   if (row0 >= R) return;
-  const int nt_used = NT == 1 ? 1 : min(per, tiles - rg * per);
   const int npages = (L + kPageSize - 1) / kPageSize;
   if (split > 0 && p_begin >= npages) return;       // empty split: the merge skips it
   const int nv = max(1, (npages + a.pages_per_split - 1) / a.pages_per_split);
   const bool direct = a.splits == 1 || nv == 1;
   const int p_end = min(npages, p_begin + a.pages_per_split);
   const int L_end = min(L, p_end * kPageSize);      // a step may reach past the split
-  const int n_w = max(0, (p_end - p_begin - NP * warp + NP * W - 1) / (NP * W));   // steps
+  const int n_w = max(0, (p_end - p0 + NP * W - 1) / (NP * W));   // steps of this warp
 
   const uint32_t bar0 = smem_u32(bars + warp * NB);
-  uint8_t* wbuf = bufs + (size_t)warp * warp_bytes(NT);
+  uint8_t* wbuf = bufs + (size_t)warp * kWarpBytes;
   const uint32_t wbuf_s = smem_u32(wbuf);
   if (lane == 0) {
 #pragma unroll
@@ -256,392 +274,380 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   }
   __syncwarp();
 
-  const uint64_t policy = l2_policy_evict_first();
+  // a cache read by several row groups should stay in L2 for them
+  const uint64_t policy = a.row_groups == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
   int ids = 0;
-  auto checked = [&](int id, int page) {            // 0 for what is not to be read
-    if (page >= p_end) return 0;
-    if (id < 0 || id >= a.num_pages) {
-      atomicOr(&g_err_int4, kErrBadIndex);
-      return 0;
-    }
-    return id;
-  };
   const uint8_t* k_head = a.k + (size_t)h * kInt4Slab;
   const uint8_t* v_head = a.v + (size_t)h * kInt4Slab;
-  const size_t page_stride = (size_t)a.num_kv_heads * kInt4Slab;
-  auto issue = [&](int j) {
+  const uint32_t page_stride = (uint32_t)a.num_kv_heads * kInt4Slab;
+  auto issue = [&](int j, int t) {                  // step j as the ring's t-th
     constexpr int kSteps = 32 / NP;                 // steps of an id word
     if (j % kSteps == 0) {
       const int pg = id_page(j);
-      ids = checked(j == 0 ? bt_first : (pg < p_end ? __ldg(bt_row + pg) : 0), pg);
+      ids = j == 0 ? bt_first : (pg < p_end ? __ldg(bt_row + pg) : 0);
+      if (pg >= p_end) ids = 0;                     // past the split: any page, never used
+      if (ids < 0 || ids >= a.num_pages) {
+        atomicOr(&g_err_int4, kErrBadIndex);
+        ids = 0;
+      }
     }
     int id[NP];
 #pragma unroll
     for (int u = 0; u < NP; ++u) id[u] = __shfl_sync(FULL, ids, (j % kSteps) * NP + u);
     if (lane == 0) {
-      const int k = j % NB;
-      const uint32_t bar = bar0 + 8 * k, dst = wbuf_s + k * (NP * kPageBytes);
-      const int n = min(NP, p_end - (p_begin + NP * (warp + j * W)));
+      const uint32_t bar = bar0 + 8 * (t % NB), dst = wbuf_s + (t % NB) * kStepBytes;
       // the warp's reads of this buffer are done (__syncwarp); order them
       // before the async-proxy refill
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive_expect_tx(bar, n * kPageBytes);
+      mbar_arrive_expect_tx(bar, kStepBytes);
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        if (u >= n) break;
-        bulk_g2s_hint(dst + u * kPageBytes, k_head + id[u] * page_stride, kInt4Slab, bar, policy);
-        bulk_g2s_hint(dst + u * kPageBytes + kInt4Slab, v_head + id[u] * page_stride, kInt4Slab,
-                      bar, policy);
+        const uint64_t at = (uint64_t)(uint32_t)id[u] * page_stride;
+        bulk_g2s_hint(dst + u * kPageBytes, k_head + at, kInt4Slab, bar, policy);
+        bulk_g2s_hint(dst + u * kPageBytes + kInt4Slab, v_head + at, kInt4Slab, bar, policy);
       }
     }
   };
   const int pro = min(NB, n_w);
-  for (int j = 0; j < pro; ++j) issue(j);
-  int issued = pro;
+  for (int j = 0; j < pro; ++j) issue(j, j);
 
-  // Query fragments (column r of n-tile nt = row row0 + 8 nt + r) and, for
-  // this lane's accumulator columns 2 qd + e, the factor from raw scores to
-  // the log2 domain (never negative: the scale's sign is in the query) and the
-  // last position the row sees.
-  uint32_t qh[NT == 1 ? 8 : 1][2], ql[NT == 1 && SMOOTH ? 8 : 1][2], off[NT];
-  uint2* qs = reinterpret_cast<uint2*>(smem + 1024);      // [hi | lo][nt][k-step][lane]
-  float sl2[NT][2];
-  int lim[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    uint32_t hi[8][2], lo[SMOOTH ? 8 : 1][2];
-    const int rq = row0 + 8 * nt + r;
+  // Query fragments (column r of the n-tile = row row0 + r; kLowBeside: columns
+  // 4-7 are the low parts of rows 0-3), made by one warp for all.
+  if (warp == W - 1) {
+    uint32_t hi[8][2], lo[LOW ? 8 : 1][2], off;
+    const int rq = row0 + (LOW == kLowBeside ? r & 3 : r);
     const __nv_bfloat16* q =
         rq < R ? a.q + ((size_t)(q0 + rq / G) * Hq + h * G + rq % G) * kHeadDim : nullptr;
     const float back =
-        query_frags<SMOOTH>(q, a.k_smooth, a.softmax_scale < 0.f ? -1.f : 1.f, qd, hi, lo, off[nt]);
-    if constexpr (NT == 1) {
+        query_frags<LOW>(q, a.k_smooth, a.softmax_scale < 0.f ? -1.f : 1.f, qd, hi, lo, off);
+    const bool low = LOW == kLowBeside && r >= 4;
+    s_off[lane] = low ? 0u : off;
+    if (qd == 0) s_back[r] = back;
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        qh[ks][0] = hi[ks][0];
-        qh[ks][1] = hi[ks][1];
-        if constexpr (SMOOTH) {
-          ql[ks][0] = lo[ks][0];
-          ql[ks][1] = lo[ks][1];
-        }
-      }
-    } else if (nt % W == warp) {
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        qs[(nt * 8 + ks) * 32 + lane] = make_uint2(hi[ks][0], hi[ks][1]);
-        if constexpr (SMOOTH)
-          qs[((NT + nt) * 8 + ks) * 32 + lane] = make_uint2(lo[ks][0], lo[ks][1]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rho = row0 + 8 * nt + 2 * qd + e;
-      // raw scores are in units of 2^-24
-      sl2[nt][e] = fabsf(a.softmax_scale) * (kLog2e * 16777216.f) *
-                   __shfl_sync(FULL, back, (2 * qd + e) * 4);
-      lim[nt][e] = min(L_end - 1, rho < R ? L - qn + rho / G : L - 1);
+    for (int ks = 0; ks < 8; ++ks) {
+      qs[ks * 32 + lane] =
+          low ? make_uint2(lo[LOW ? ks : 0][0], lo[LOW ? ks : 0][1]) : make_uint2(hi[ks][0], hi[ks][1]);
+      if constexpr (LOW == kLowApart) qs[(8 + ks) * 32 + lane] = make_uint2(lo[ks][0], lo[ks][1]);
     }
   }
-  if constexpr (NT > 1) __syncthreads();
-  int lim_min = L_end - 1;                          // steps up to it need no mask
+  __syncthreads();
+  // For this lane's accumulator columns 2 qd + e: the factor from raw scores (in
+  // units of 2^-24) to the log2 domain, never negative (the scale's sign is in
+  // the query), and the last position the row sees.
+  const uint32_t off = s_off[lane];
+  float sl2[2];
+  int lim[2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) lim_min = min(lim_min, min(lim[nt][0], lim[nt][1]));
-  lim_min = __reduce_min_sync(FULL, lim_min);
+  for (int e = 0; e < 2; ++e) {
+    const int c = 2 * qd + e, rho = row0 + (LOW == kLowBeside ? c & 3 : c);
+    sl2[e] = fabsf(a.softmax_scale) * (kLog2e * 16777216.f) * s_back[c];
+    lim[e] = min(L_end - 1, rho < R ? L - qn + rho / G : L - 1);
+  }
+  // steps whose keys all rows see: the first n_full
+  const int lim_min = __reduce_min_sync(FULL, min(L_end - 1, min(lim[0], lim[1])));
+  const int spare = lim_min + 1 - p0 * kPageSize;   // keys that all see, from step 0 on
+  const int n_full = min(n_w, max(0, (spare + (W - 1) * kStepKeys) / (W * kStepKeys)));
 
-  auto q_frag = [&](int nt, int ks, bool low) -> uint2 {
-    if constexpr (NT == 1) {
-      if constexpr (SMOOTH)
-        return low ? make_uint2(ql[ks][0], ql[ks][1]) : make_uint2(qh[ks][0], qh[ks][1]);
-      else
-        return make_uint2(qh[ks][0], qh[ks][1]);
-    } else {
-      return qs[(((low ? NT : 0) + nt) * 8 + ks) * 32 + lane];
-    }
-  };
-
-  // O^T of n-tile nt, group g, half t: channels 32 g + 4 r + 2 t (o[..][0..1])
-  // and + 1 (o[..][2..3], times 16) of columns 2 qd, 2 qd + 1, in units of
-  // 2^-24 and with the codes' offset of 8; cs: 8 sum(P') of group r / 2.
-  // mu: the maximum the exponentials are taken against; p carries 2^(kShift -
-  // vexp), where every V scale so far is below 2^vexp.
-  float o[NT][8][4], cs[NT][4];
-  float mu[NT][2], l[NT][2];
-  int vexp = 0;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  // O^T of group g, half t: channels 32 g + 4 r + 2 t (o[..][0..1]) and + 1
+  // (o[..][2..3], times 16) of columns 2 qd, 2 qd + 1, in units of 2^-24 and with
+  // the codes' offset of 8; cs[g2]: 8 sum(P') of groups 2 g2 ([0..1]) and 2 g2 + 1
+  // ([2..3]).  mu: the maximum the exponentials are taken against; p carries
+  // 2^(kShift - vexp); sub = kShift - vexp - mu.
+  float o[8][4], cs[2][4], mu[2], sub[2], l[2];
+  int vexp, vtop;
+  auto reset = [&]() {
+    vexp = 0;
+    vtop = -14;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[nt][t][j] = 0.f;
+      for (int j = 0; j < 4; ++j) o[t][j] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cs[nt][j] = 0.f;
-    mu[nt][0] = mu[nt][1] = kNoKey;
-    l[nt][0] = l[nt][1] = 0.f;
-  }
-  auto rescale = [&](int nt, float a0, float a1) {
+    for (int j = 0; j < 4; ++j) cs[0][j] = cs[1][j] = 0.f;
+    mu[0] = mu[1] = kNoKey;
+    sub[0] = sub[1] = (float)kShift - kNoKey;
+    l[0] = l[1] = 0.f;
+  };
+  auto rescale = [&](float a0, float a1) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      o[nt][q][0] *= a0;
-      o[nt][q][2] *= a0;
-      o[nt][q][1] *= a1;
-      o[nt][q][3] *= a1;
+      o[q][0] *= a0;
+      o[q][2] *= a0;
+      o[q][1] *= a1;
+      o[q][3] *= a1;
     }
-    cs[nt][0] *= a0;
-    cs[nt][1] *= a1;
-    l[nt][0] *= a0;
-    l[nt][1] *= a1;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      cs[q][0] *= a0;
+      cs[q][2] *= a0;
+      cs[q][1] *= a1;
+      cs[q][3] *= a1;
+    }
+    l[0] *= a0;
+    l[1] *= a1;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) sub[e] = (float)(kShift - vexp) - mu[e];
   };
+  auto raise_vexp = [&](int now) {
+    const float f = __int_as_float((127 + vexp - now) << 23);
+    vexp = now;
+    rescale(f, f);
+  };
+  float zero[4];                                    // opaque, so that they stay in registers
+#pragma unroll
+  for (int j = 0; j < 4; ++j) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[j]));
+  // slot order of the MMA rows: row i = slot 2 i, row 8 + i = slot 2 i + 1, so
+  // that a lane's scales are 16 contiguous bytes
+  const int ld_row = (lane >> 4) * 256 + (2 * (lane & 7) + ((lane >> 3) & 1)) * 16;
 
   // One step: the NP pages in the buffer at kb, whose first key is key0.
-  // MASKED: it holds the causal edge or the end of the sequence or the split.
-  auto step = [&](const uint8_t* kb, uint32_t kst, int key0, auto masked_tag) {
-    constexpr bool MASKED = decltype(masked_tag)::value;
-    // V scales of keys 2 qd, 2 qd + 1 (a) and + 8 (b): words (g0 g1, g2 g3) of
-    // each; slots past the sequence may hold anything
+  // CAREFUL: it may hold the causal edge or the end of the sequence or the
+  // split (slots past it may hold anything), and the V scales are watched.
+  auto step = [&](const uint8_t* kb, uint32_t kst, int key0, auto careful_tag) {
+    constexpr bool CAREFUL = decltype(careful_tag)::value;
+    // raw scores s = sum_g scale (sum u q - 8 sum q) of slots 2 r and 2 r + 1
+    float s[NP][4];
+    uint2 ks0[NP], ks1[NP];
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const uint8_t* sc = kb + u * kPageBytes + kInt4Codes;
+      const uint4 both = *reinterpret_cast<const uint4*>(sc + r * 16);      // slots 2 r, 2 r + 1
+      ks0[u] = make_uint2(both.x, both.y);
+      ks1[u] = make_uint2(both.z, both.w);
+      mma_f16_new(s[u], (qd & 1) ? both.y : both.x, (qd & 1) ? both.w : both.z, 0u, 0u, off, 0u,
+                  zero);
+    }
+#pragma unroll
+    for (int g2 = 0; g2 < 2; ++g2) {
+      uint32_t kw[NP][4];            // slots 2 r, 2 r + 1 of group 2 g2, then of 2 g2 + 1
+#pragma unroll
+      for (int u = 0; u < NP; ++u) ldsm_x4(kst + u * kPageBytes + g2 * 512 + ld_row, kw[u]);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int g = 2 * g2 + w;
+        const uint2 qa = qs[(2 * g) * 32 + lane], qb = qs[(2 * g + 1) * 32 + lane];
+        uint2 la = make_uint2(0u, 0u), lb = la;
+        if constexpr (LOW == kLowApart) {
+          la = qs[(8 + 2 * g) * 32 + lane];
+          lb = qs[(9 + 2 * g) * 32 + lane];
+        }
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {
+          const uint32_t w0 = kw[u][2 * w], w1 = kw[u][2 * w + 1];
+          const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
+          const float2 fa = halves(g2 ? ks0[u].y : ks0[u].x), fb = halves(g2 ? ks1[u].y : ks1[u].x);
+          const float f0 = w ? fa.y : fa.x, f1 = w ? fb.y : fb.x;
+          float d[4];
+          mma_f16_new(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, qa.x, qa.y, zero);
+          mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, qb.x, qb.y);
+          if constexpr (LOW == kLowApart) {
+            mma_f16(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, la.x, la.y);
+            mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, lb.x, lb.y);
+          }
+          s[u][0] = fmaf(f0, d[0], s[u][0]);
+          s[u][1] = fmaf(f0, d[1], s[u][1]);
+          s[u][2] = fmaf(f1, d[2], s[u][2]);
+          s[u][3] = fmaf(f1, d[3], s[u][3]);
+        }
+      }
+    }
+    if constexpr (LOW == kLowBeside) {                 // high + low columns, in both
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[u][j] += __shfl_xor_sync(FULL, s[u][j], 2);
+    }
+
+    // V scales of slots 4 qd, 4 qd + 1 (va) and + 2, + 3 (vb): words (g0 g1,
+    // g2 g3) of each
     uint4 va[NP], vb[NP];
     uint32_t vm = 0;
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const uint8_t* sc = kb + u * kPageBytes + kInt4Slab + kInt4Codes;
-      va[u] = *reinterpret_cast<const uint4*>(sc + qd * 16);
-      vb[u] = *reinterpret_cast<const uint4*>(sc + 64 + qd * 16);
-      if constexpr (MASKED) {
-        const int left = L_end - (key0 + u * kPageSize + 2 * qd);     // valid from this lane's first key on
+      va[u] = *reinterpret_cast<const uint4*>(sc + qd * 32);
+      vb[u] = *reinterpret_cast<const uint4*>(sc + qd * 32 + 16);
+      if constexpr (CAREFUL) {
+        const int left = L_end - (key0 + u * kPageSize + 4 * qd);   // valid slots from 4 qd on
         if (left <= 0) va[u].x = va[u].y = 0u;
         if (left <= 1) va[u].z = va[u].w = 0u;
-        if (left <= 8) vb[u].x = vb[u].y = 0u;
-        if (left <= 9) vb[u].z = vb[u].w = 0u;
+        if (left <= 2) vb[u].x = vb[u].y = 0u;
+        if (left <= 3) vb[u].z = vb[u].w = 0u;
+        vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(va[u].x, va[u].y), __vmaxu2(va[u].z, va[u].w)));
+        vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(vb[u].x, vb[u].y), __vmaxu2(vb[u].z, vb[u].w)));
       }
-      vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(va[u].x, va[u].y), __vmaxu2(va[u].z, va[u].w)));
-      vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(vb[u].x, vb[u].y), __vmaxu2(vb[u].z, vb[u].w)));
     }
-    // a scale of 2^vexp or more (its fp16 exponent field E: scale < 2^(E - 14))
-    const int ve = (int)(max(vm & 0xffffu, vm >> 16) >> 10) - 14;
-    if (__any_sync(FULL, ve > vexp)) {
-      const int now = __reduce_max_sync(FULL, ve);
-      const float f = __int_as_float((127 + vexp - now) << 23);
-      vexp = now;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) rescale(nt, f, f);
+    if constexpr (CAREFUL) {
+      // keep every V scale below 2^vexp (fp16 exponent field E: scale < 2^(E - 14))
+      vtop = max(vtop, __reduce_max_sync(FULL, (int)(max(vm & 0xffffu, vm >> 16) >> 10) - 14));
+      if (vtop > vexp) raise_vexp(vtop);
     }
 
-    // raw scores s = sum_g scale (sum u q - 8 sum q) of keys r and r + 8
-    float s[NP][NT][4];
+    // softmax; P of a page as the B fragment's two words (slots 4 qd, 4 qd + 2
+    // and 4 qd + 1, 4 qd + 3 of row r), in f16
+    auto sees = [&](int u, int j) { return key0 + u * kPageSize + 2 * r + (j >> 1) <= lim[j & 1]; };
+    float pm[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int u = 0; u < NP; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (!CAREFUL || sees(u, j)) pm[j & 1] = fmaxf(pm[j & 1], s[u][j]);
+#pragma unroll
+    for (int x = 4; x <= 16; x <<= 1) {
+      pm[0] = fmaxf(pm[0], __shfl_xor_sync(FULL, pm[0], x));
+      pm[1] = fmaxf(pm[1], __shfl_xor_sync(FULL, pm[1], x));
+    }
+    // the maximum moves only when a step passes it by more than 8
+    pm[0] *= sl2[0];
+    pm[1] *= sl2[1];
+    const bool up0 = pm[0] > mu[0] + 8.f, up1 = pm[1] > mu[1] + 8.f;
+    if (__any_sync(FULL, up0 || up1)) {
+      const float f0 = up0 ? fast_exp2(mu[0] - pm[0]) : 1.f;
+      const float f1 = up1 ? fast_exp2(mu[1] - pm[1]) : 1.f;
+      if (up0) mu[0] = pm[0];
+      if (up1) mu[1] = pm[1];
+      rescale(f0, f1);
+    }
+    uint32_t pw[NP][2];
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-      const uint8_t* kc = kb + u * kPageBytes;
-      const uint32_t kcs = kst + u * kPageBytes;
-      const uint2 ks0 = *reinterpret_cast<const uint2*>(kc + kInt4Codes + r * 8);
-      const uint2 ks1 = *reinterpret_cast<const uint2*>(kc + kInt4Codes + r * 8 + 64);
-      const uint32_t t0 = (qd & 1) ? ks0.y : ks0.x, t1 = (qd & 1) ? ks1.y : ks1.x;
+      float p[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
-        mma_f16(s[u][nt], t0, t1, 0u, 0u, off[nt], 0u);
+      for (int j = 0; j < 4; ++j) {
+        p[j] = fast_exp2(fmaf(s[u][j], sl2[j & 1], sub[j & 1]));
+        if (CAREFUL && !sees(u, j)) p[j] = 0.f;
       }
-#pragma unroll
-      for (int g2 = 0; g2 < 2; ++g2) {
-        uint32_t kw[4];              // group 2 g2: keys r, r + 8; group 2 g2 + 1: the same
-        ldsm_x4(kcs + g2 * 512 + lane * 16, kw);
-        const float2 fa = halves(g2 ? ks0.y : ks0.x), fb = halves(g2 ? ks1.y : ks1.x);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int g = 2 * g2 + w;
-          const uint32_t w0 = kw[2 * w], w1 = kw[2 * w + 1];
-          const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
-          const float f0 = w ? fa.y : fa.x, f1 = w ? fb.y : fb.x;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && nt >= nt_used) break;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint2 qa = q_frag(nt, 2 * g, false), qb = q_frag(nt, 2 * g + 1, false);
-            mma_f16(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, qa.x, qa.y);
-            mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, qb.x, qb.y);
-            if constexpr (SMOOTH) {
-              const uint2 la = q_frag(nt, 2 * g, true), lb = q_frag(nt, 2 * g + 1, true);
-              mma_f16(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, la.x, la.y);
-              mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, lb.x, lb.y);
-            }
-            s[u][nt][0] = fmaf(f0, d[0], s[u][nt][0]);
-            s[u][nt][1] = fmaf(f0, d[1], s[u][nt][1]);
-            s[u][nt][2] = fmaf(f1, d[2], s[u][nt][2]);
-            s[u][nt][3] = fmaf(f1, d[3], s[u][nt][3]);
-          }
-        }
-      }
+      l[0] += p[0] + p[2];
+      l[1] += p[1] + p[3];
+      pw[u][0] = movm_t(pack_f16x2(p[0], p[1]));
+      pw[u][1] = movm_t(pack_f16x2(p[2], p[3]));
     }
 
-    // softmax; P of a page as the B fragment's two words (keys 2 qd, 2 qd + 1
-    // and + 8 of head r), in f16
-    uint32_t pw[NP][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (NT > 1 && nt >= nt_used) break;
-      auto sees = [&](int u, int j) {
-        return key0 + u * kPageSize + r + (j < 2 ? 0 : 8) <= lim[nt][j & 1];
-      };
-      float pm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int u = 0; u < NP; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (MASKED) {
-            if (sees(u, j)) pm[j & 1] = fmaxf(pm[j & 1], s[u][nt][j]);
-          } else {
-            pm[j & 1] = fmaxf(pm[j & 1], s[u][nt][j]);
-          }
-        }
-#pragma unroll
-      for (int x = 4; x <= 16; x <<= 1) {
-        pm[0] = fmaxf(pm[0], __shfl_xor_sync(FULL, pm[0], x));
-        pm[1] = fmaxf(pm[1], __shfl_xor_sync(FULL, pm[1], x));
-      }
-      // the maximum moves only when a step passes it by more than 8
-      pm[0] *= sl2[nt][0];
-      pm[1] *= sl2[nt][1];
-      const bool g0 = pm[0] > mu[nt][0] + 8.f, g1 = pm[1] > mu[nt][1] + 8.f;
-      if (__any_sync(FULL, g0 || g1)) {
-        const float a0 = g0 ? fast_exp2(mu[nt][0] - pm[0]) : 1.f;
-        const float a1 = g1 ? fast_exp2(mu[nt][1] - pm[1]) : 1.f;
-        if (g0) mu[nt][0] = pm[0];
-        if (g1) mu[nt][1] = pm[1];
-        rescale(nt, a0, a1);
-      }
-      const float sub0 = kShift - (float)vexp - mu[nt][0], sub1 = kShift - (float)vexp - mu[nt][1];
-#pragma unroll
-      for (int u = 0; u < NP; ++u) {
-        float p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          p[j] = fast_exp2(fmaf(s[u][nt][j], sl2[nt][j & 1], (j & 1) ? sub1 : sub0));
-          if constexpr (MASKED) {
-            if (!sees(u, j)) p[j] = 0.f;
-          }
-        }
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
-        pw[u][nt][0] = movm_t(pack_f16x2(p[0], p[1]));
-        pw[u][nt][1] = movm_t(pack_f16x2(p[2], p[3]));
-      }
-    }
-
-    // O += V P', group by group
+    // O += V P', cs += 8 P', group by group
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const uint32_t vcs = kst + u * kPageBytes + kInt4Slab;
 #pragma unroll
       for (int g2 = 0; g2 < 2; ++g2) {
         uint32_t vw[4];
-        ldsm_x4_t(vcs + g2 * 512 + lane * 16, vw);
+        ldsm_x4_t(vcs + g2 * 512 + ld_row, vw);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int g = 2 * g2 + w;
           const uint32_t w0 = vw[2 * w], w1 = vw[2 * w + 1];
           const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
-          const uint32_t sel = w ? 0x7632u : 0x5410u;    // group g of two keys' words
-          const uint32_t sa = __byte_perm(g2 ? va[u].y : va[u].x, g2 ? va[u].w : va[u].z, sel);
-          const uint32_t sb = __byte_perm(g2 ? vb[u].y : vb[u].x, g2 ? vb[u].w : vb[u].z, sel);
-          const uint32_t eight = (r >> 1) == g ? 0x00080008u : 0u;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && nt >= nt_used) break;
-            const uint32_t pb0 = mul_f16x2(pw[u][nt][0], sa), pb1 = mul_f16x2(pw[u][nt][1], sb);
-            mma_f16(o[nt][2 * g], w0 & NIB0, w0 & NIB1, w1 & NIB0, w1 & NIB1, pb0, pb1);
-            mma_f16(o[nt][2 * g + 1], x0 & NIB0, x0 & NIB1, x1 & NIB0, x1 & NIB1, pb0, pb1);
-            mma_f16(cs[nt], eight, 0u, eight, 0u, pb0, pb1);
-          }
+          const uint32_t sel = w ? 0x7632u : 0x5410u;    // group g of two slots' words
+          const uint32_t sa = __byte_perm(g2 ? va[u].y : va[u].x, g2 ? vb[u].y : vb[u].x, sel);
+          const uint32_t sb = __byte_perm(g2 ? va[u].w : va[u].z, g2 ? vb[u].w : vb[u].z, sel);
+          const uint32_t pb0 = mul_f16x2(pw[u][0], sa), pb1 = mul_f16x2(pw[u][1], sb);
+          mma_f16(o[2 * g], w0 & NIB0, w0 & NIB1, w1 & NIB0, w1 & NIB1, pb0, pb1);
+          mma_f16(o[2 * g + 1], x0 & NIB0, x0 & NIB1, x1 & NIB0, x1 & NIB1, pb0, pb1);
+          mma_f16(cs[g2], w ? 0u : kEight, w ? kEight : 0u, w ? 0u : kEight, w ? kEight : 0u, pb0,
+                  pb1);
         }
       }
     }
   };
 
+  // The first step watches the V scales and leaves kMargin octaves for the
+  // others, whose P' stays finite unless a scale outgrows them and its key's p
+  // is near the top.  If O is not finite at the end, a second pass watches
+  // every step (a NaN in the cache costs that pass too).
+  int t = 0, t_issued = pro;                        // steps taken from and put into the ring
   bool failed = false;
-  int j_fail = 0;
-  for (int j = 0; j < n_w; ++j) {
-    const int k = j % NB;
-    if (!__all_sync(FULL, mbar_wait(bar0 + 8 * k, (uint32_t)(j / NB) & 1u))) {
+  // step j: waits for its buffer, works on it and refills it with step j + NB
+  auto take = [&](int j, auto careful_tag) {
+    if (!__all_sync(FULL, mbar_wait(bar0 + 8 * (t % NB), (uint32_t)(t / NB) & 1u))) {
       failed = true;
-      j_fail = j;
-      break;
+      return;
     }
-    const int key0 = (p_begin + NP * (warp + j * W)) * kPageSize;
-    const int at = k * (NP * kPageBytes);
-    if (key0 + NP * kPageSize - 1 <= lim_min)
-      step(wbuf + at, wbuf_s + at, key0, std::false_type{});
-    else
-      step(wbuf + at, wbuf_s + at, key0, std::true_type{});
+    const int at = (t % NB) * kStepBytes;
+    step(wbuf + at, wbuf_s + at, (p0 + NP * W * j) * kPageSize, careful_tag);
     __syncwarp();
-    if (issued < n_w) issue(issued++);
+    if (j + NB < n_w) issue(j + NB, t_issued++);
+    ++t;
+  };
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    reset();
+    if (pass > 0)
+      for (int j = 0; j < pro; ++j) issue(j, t_issued++);
+    int j = 0;
+    if (pass == 0 && n_full > 1) {
+      take(0, std::true_type{});
+      if (vtop + kMargin > vexp) raise_vexp(min(17, vtop + kMargin));
+#pragma unroll 1
+      for (j = 1; j < n_full && !failed; ++j) take(j, std::false_type{});
+    }
+#pragma unroll 1
+    for (; j < n_w && !failed; ++j) take(j, std::true_type{});
+    if (failed) break;
+    bool finite = true;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) finite = finite && fabsf(o[q][i]) < INFINITY;
+    if (__all_sync(FULL, finite)) break;
   }
   if (failed) {
     if (lane == 0) atomicOr(&g_err_int4, kErrTimeout);
     // let every copy this warp issued land (bounded) before the buffers are
     // reused or the CTA exits
-    for (int j = j_fail; j < issued; ++j)
-      (void)mbar_wait(bar0 + 8 * (j % NB), (uint32_t)(j / NB) & 1u);
+    for (; t < t_issued; ++t) (void)mbar_wait(bar0 + 8 * (t % NB), (uint32_t)(t / NB) & 1u);
   }
   __syncwarp();
 
   // Park (O unnormalised, m, l) of the warp's rows in its buffers (all of its
-  // copies have landed): O [8 NT][128], m [8 NT], l [8 NT]; m is where p = 1.
+  // copies have landed): O [8][128], m [8], l [8]; m is where p = 2^kShift.
   float* wo = reinterpret_cast<float*>(wbuf);
-  float* wm = wo + 8 * NT * kHeadDim;
-  float* wl = wm + 8 * NT;
+  float* wm = wo + kRows * kHeadDim;
+  float* wl = wm + kRows;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int x = 4; x <= 16; x <<= 1) {
+    l[0] += __shfl_xor_sync(FULL, l[0], x);
+    l[1] += __shfl_xor_sync(FULL, l[1], x);
+  }
 #pragma unroll
-    for (int x = 4; x <= 16; x <<= 1) {
-      l[nt][0] += __shfl_xor_sync(FULL, l[nt][0], x);
-      l[nt][1] += __shfl_xor_sync(FULL, l[nt][1], x);
+  for (int g = 0; g < 4; ++g)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      constexpr float k24 = 16777216.f, k20 = 1048576.f;
+      const float kk = cs[g >> 1][2 * (g & 1) + e];
+      float4 v = make_float4(o[2 * g][e] * k24 - kk, o[2 * g][2 + e] * k20 - kk,
+                             o[2 * g + 1][e] * k24 - kk, o[2 * g + 1][2 + e] * k20 - kk);
+      if (failed) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(wo + (2 * qd + e) * kHeadDim + 32 * g + 4 * r) = v;
     }
+  if (r == 0) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float k0 = __shfl_sync(FULL, cs[nt][0], 8 * g + qd);
-      const float k1 = __shfl_sync(FULL, cs[nt][1], 8 * g + qd);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float* row = wo + (8 * nt + 2 * qd + e) * kHeadDim + 32 * g + 4 * r;
-        const float kk = e ? k1 : k0;
-        float4 v = make_float4((o[nt][2 * g][e] - kk) * 16777216.f,
-                               (o[nt][2 * g][2 + e] * 0.0625f - kk) * 16777216.f,
-                               (o[nt][2 * g + 1][e] - kk) * 16777216.f,
-                               (o[nt][2 * g + 1][2 + e] * 0.0625f - kk) * 16777216.f);
-        if (failed) v = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(row) = v;
-      }
-    }
-    if (r == 0) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool none = failed || mu[nt][e] == kNoKey;
-        wm[8 * nt + 2 * qd + e] = none ? kNoKey : mu[nt][e] + (float)vexp;
-        wl[8 * nt + 2 * qd + e] = failed ? 0.f : l[nt][e];
-      }
+    for (int e = 0; e < 2; ++e) {
+      const bool none = failed || mu[e] == kNoKey;
+      wm[2 * qd + e] = none ? kNoKey : mu[e] + (float)vexp;
+      wl[2 * qd + e] = failed ? 0.f : l[e];
     }
   }
   __syncthreads();
 
   // Merge the warps (log-sum-exp rule); write the bf16 output (one split) or
   // the split's partial.
-  constexpr size_t kStride = warp_bytes(NT);
-  const int rows = min(8 * nt_used, R - row0);
-  for (int t = threadIdx.x; t < rows * kHeadDim; t += W * 32) {
-    const int n = t / kHeadDim, d = t % kHeadDim;
+  const int rows = min(kRows, R - row0);
+  for (int i = threadIdx.x; i < rows * kHeadDim; i += W * 32) {
+    const int n = i / kHeadDim, d = i % kHeadDim;
     float M = kNoKey;
 #pragma unroll
     for (int w = 0; w < W; ++w)
-      M = fmaxf(M, reinterpret_cast<const float*>(bufs + w * kStride)[8 * NT * kHeadDim + n]);
+      M = fmaxf(M, reinterpret_cast<const float*>(bufs + w * kWarpBytes)[kRows * kHeadDim + n]);
     float Ls = 0.f, O = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float* x = reinterpret_cast<const float*>(bufs + w * kStride);
-      const float f = fast_exp2(x[8 * NT * kHeadDim + n] - M);
-      Ls += f * x[8 * NT * (kHeadDim + 1) + n];
+      const float* x = reinterpret_cast<const float*>(bufs + w * kWarpBytes);
+      const float f = fast_exp2(x[kRows * kHeadDim + n] - M);
+      Ls += f * x[kRows * (kHeadDim + 1) + n];
       O += f * x[n * kHeadDim + d];
     }
     const bool none = Ls == 0.f;                    // no key seen
     O = none ? 0.f : O / Ls;
-    const float lse2 = none ? -INFINITY : M - kShift + fast_log2(Ls);
+    const float lse2 = none ? -INFINITY : M - (float)kShift + fast_log2(Ls);
     const int rho = row0 + n;
     const size_t bh = (size_t)(q0 + rho / G) * Hq + h * G + rho % G;
     if (direct) {
@@ -664,7 +670,7 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     uint32_t old;
     asm volatile("fence.acq_rel.gpu;\n\tatom.relaxed.gpu.global.add.u32 %0, [%1], 1;"
                  : "=r"(old) : "l"(ctr) : "memory");
-    const bool last = old == (uint32_t)(nv * ((tiles + per - 1) / per)) - 1u;
+    const bool last = old == (uint32_t)(nv * ((R + kRows - 1) / kRows)) - 1u;
     if (last) {
       asm volatile("fence.acq_rel.gpu;" ::: "memory");
       *ctr = 0u;
@@ -687,32 +693,21 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   }
 }
 
-template <int NT, bool SMOOTH>
+template <int LOW>
 cudaError_t launch_as(const Launch& a, int batch, cudaStream_t s) {
-  const int smem = smem_of(NT, SMOOTH);
+  constexpr int smem = smem_of(LOW);
   cudaError_t e = pkv_host::set_max_dynamic_smem(
-      reinterpret_cast<const void*>(decode_int4_kernel<NT, SMOOTH>), smem);
+      reinterpret_cast<const void*>(decode_int4_kernel<LOW>), smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.splits, a.num_kv_heads * a.row_groups, batch);
-  decode_int4_kernel<NT, SMOOTH><<<grid, W * 32, smem, s>>>(a);
+  decode_int4_kernel<LOW><<<grid, W * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int NT>
-cudaError_t launch_nt(const Launch& a, int batch, cudaStream_t s) {
-  return a.k_smooth ? launch_as<NT, true>(a, batch, s) : launch_as<NT, false>(a, batch, s);
-}
-
-// The n-tiles of 8 rows that cover `rows` in as few CTAs as hold them.
 cudaError_t launch_rows(Launch& a, int rows, int batch, cudaStream_t s) {
-  const int tiles = (rows + 7) / 8;
-  a.row_groups = (tiles + 3) / 4;
-  switch ((tiles + a.row_groups - 1) / a.row_groups) {
-    case 1: return launch_nt<1>(a, batch, s);
-    case 2: return launch_nt<2>(a, batch, s);
-    case 3: return launch_nt<3>(a, batch, s);
-    default: return launch_nt<4>(a, batch, s);
-  }
+  a.row_groups = (rows + kRows - 1) / kRows;
+  if (!a.k_smooth) return launch_as<kPlain>(a, batch, s);
+  return rows <= kRows / 2 ? launch_as<kLowBeside>(a, batch, s) : launch_as<kLowApart>(a, batch, s);
 }
 
 }  // namespace
