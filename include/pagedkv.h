@@ -359,10 +359,17 @@ pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int3
 
 /*
  * paged_attn_decode_multi_int4 -- the same on a PKV_INT4 pool
- * (PKV_ERR_UNSUPPORTED for others).  Plan, workspace and arguments as
- * pkv_paged_attn_decode_multi's; k_smooth: the fp32 [128] weight given to
- * kv_append (16-byte aligned), or NULL.
+ * (PKV_ERR_UNSUPPORTED for others).  Arguments as
+ * pkv_paged_attn_decode_multi's, the workspace as pkv_decode_multi_int4_plan's;
+ * k_smooth: the fp32 [128] weight given to kv_append (16-byte aligned), or
+ * NULL.
  */
+pkv_status pkv_decode_multi_int4_plan(int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t max_q_len,
+                                      int32_t max_seq_len, int32_t num_splits,
+                                      int32_t* splits_out, int32_t* pages_per_split_out,
+                                      size_t* workspace_bytes_out);
+
 pkv_status pkv_paged_attn_decode_multi_int4(const pkv_pool* pool, const void* q, int32_t total_q,
                                             const int32_t* cu_q, int32_t batch,
                                             int32_t num_q_heads, const int32_t* block_table,

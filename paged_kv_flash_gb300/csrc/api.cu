@@ -107,9 +107,25 @@ struct Plan {
   size_t ws_bytes, ws_zero_bytes, ws_o_offset, ws_lse_offset;
 };
 
-// quant: an INT8 or INT4 pool (longer splits, a full wave of CTAs).
+// Quantised pools: longer splits, a full wave of CTAs.  INT4 (four CTAs
+// resident per SM, eight pages a round of a CTA's warps): work that would give
+// splits of the most pages takes longer ones still where those make a single
+// wave (eight 32k-position sequences: 9 splits of 232 pages 66.8 us, 16 of 128
+// 68.6 us, 12 of 176, a wave and a quarter, 76.8 us).
+constexpr int kInt4CtasPerSm = 4, kInt4Round = 8, kInt4WaveMaxPages = 256;
+constexpr int kInt4MultiMinPages = 16;
+
+// Pages per split with which `units` work items of mp pages make one wave of
+// int4 CTAs.
+int int4_wave_pages(long long units, int mp) {
+  const long long s1 = std::max<long long>(1, (long long)sm_count() * kInt4CtasPerSm / units);
+  const long long c = (mp + s1 - 1) / s1;
+  return (int)((c + kInt4Round - 1) / kInt4Round * kInt4Round);
+}
+
 Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, int num_splits,
-               bool quant) {
+               int dtype) {
+  const bool quant = dtype != PKV_BF16;
   const int mp = std::max(1, (max_seq_len + pkv::kPageSize - 1) / pkv::kPageSize);
   int C;
   if (num_splits > 0) {
@@ -122,7 +138,13 @@ Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, in
     long long c = (page_heads + target - 1) / target;
     c = std::max<long long>(kPlanMinPages,
                             std::min<long long>(quant ? kPlanMaxPages : kPlanMaxPagesBf16, c));
-    c = (c + pkv_host::kDecodeWarps - 1) / pkv_host::kDecodeWarps * pkv_host::kDecodeWarps;
+    const int round = dtype == PKV_INT4 ? kInt4Round : pkv_host::kDecodeWarps;
+    c = (c + round - 1) / round * round;
+    if (dtype == PKV_INT4 && c >= kPlanMaxPages) {
+      const int rows = num_q_heads / num_kv_heads;      // 8 of them a CTA
+      const int wave = int4_wave_pages((long long)batch * num_kv_heads * ((rows + 7) / 8), mp);
+      if (wave <= kInt4WaveMaxPages) c = std::max<long long>(c, wave);
+    }
     C = (int)std::min<long long>(c, mp);
   }
   C = std::max(1, C);
@@ -178,8 +200,12 @@ struct MultiPlan {
   int row_groups;
 };
 
+// INT4 pools: one CTA per 8 rows, splits of 16..128 pages that make one wave
+// (a 16-token step at 1,024 positions: 4 splits of 16 pages 11.5 us, 8 of 8
+// 12.3 us; eight ragged steps at 4k..8k: 4 splits of 128 pages 85.8 us, 8 of 64
+// 94.2 us).
 MultiPlan make_multi_plan(int batch, int total_q, int num_q_heads, int num_kv_heads, int max_q,
-                          int max_seq_len, int num_splits) {
+                          int max_seq_len, int num_splits, int dtype) {
   MultiPlan m;
   const int G = num_q_heads / num_kv_heads;
   const int rows = max_q * G;
@@ -190,6 +216,11 @@ MultiPlan make_multi_plan(int batch, int total_q, int num_q_heads, int num_kv_he
   int C;
   if (num_splits > 0) {
     C = (mp + num_splits - 1) / num_splits;
+  } else if (dtype == PKV_INT4) {
+    const long long units =
+        std::max<long long>(1, (long long)batch * num_kv_heads * ((rows + 7) / 8));
+    C = std::min(mp, std::max(kInt4MultiMinPages,
+                              std::min((int)kPlanMaxPages, int4_wave_pages(units, mp))));
   } else {
     const long long slots = (long long)sm_count() * kMultiCtasPerSm;
     const long long target = std::max<long long>(1, slots * kPlanSlotsNum / kPlanSlotsDen);
@@ -257,7 +288,7 @@ pkv_status pkv_decode_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_he
     return PKV_ERR_INVALID;
   if (num_splits > 1 && (long long)batch * num_kv_heads > kDecodeCounters) return PKV_ERR_INVALID;
   const Plan p = make_plan(batch, num_q_heads, num_kv_heads, max_seq_len, num_splits,
-                           dtype != PKV_BF16);
+                           dtype);
   if (splits_out) *splits_out = p.splits;
   if (pages_per_split_out) *pages_per_split_out = p.pages_per_split;
   if (workspace_bytes_out) *workspace_bytes_out = p.ws_bytes;
@@ -344,7 +375,7 @@ static pkv_status decode_call(const pkv_pool* pool, const void* q, int32_t batch
   if (num_splits > 1 && (long long)batch * pool->num_kv_heads > kDecodeCounters)
     return PKV_ERR_INVALID;
   const Plan p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, num_splits,
-                           pool->dtype != PKV_BF16);
+                           pool->dtype);
   if (p.ws_bytes > 0 && (!workspace || workspace_bytes < p.ws_bytes || !aligned(workspace, 256)))
     return PKV_ERR_INVALID;
   if ((long long)batch > 65535 || p.splits > 2147483647 / 2) return PKV_ERR_UNSUPPORTED;
@@ -422,14 +453,14 @@ pkv_status pkv_paged_attn_decode_noalloc(const pkv_pool* pool, const void* q, in
   if (num_splits > 1 && (long long)batch * pool->num_kv_heads > kDecodeCounters)
     return PKV_ERR_INVALID;
   const size_t cap = pkv_host::decode_fixed_scratch_bytes();
-  const bool quant = pool->dtype != PKV_BF16;
-  Plan p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, num_splits, quant);
+  Plan p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, num_splits,
+                     pool->dtype);
   if (p.ws_bytes > cap) {
     if (num_splits > 0) return PKV_ERR_INVALID;       // forced split count does not fit
     int s = p.splits;
     while (s > 1 && p.ws_bytes > cap) {
       --s;
-      p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, s, quant);
+      p = make_plan(batch, num_q_heads, pool->num_kv_heads, max_seq_len, s, pool->dtype);
     }
     if (p.ws_bytes > cap) return PKV_ERR_INVALID;
   }
@@ -554,20 +585,39 @@ pkv_status pkv_qkv_norm_rope_append(const pkv_pool* pool, const void* qkv, int32
   return cuda_status(pkv_host::launch_qkv_prep(a, static_cast<cudaStream_t>(stream)));
 }
 
-pkv_status pkv_decode_multi_plan(int32_t batch, int32_t total_q, int32_t num_q_heads,
-                                 int32_t num_kv_heads, int32_t max_q_len, int32_t max_seq_len,
-                                 int32_t num_splits, int32_t* splits_out,
-                                 int32_t* pages_per_split_out, size_t* workspace_bytes_out) {
+static pkv_status multi_plan_call(int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t max_q_len, int32_t max_seq_len,
+                                  int32_t num_splits, int32_t dtype, int32_t* splits_out,
+                                  int32_t* pages_per_split_out, size_t* workspace_bytes_out) {
   if (batch < 0 || total_q < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       num_q_heads % num_kv_heads || max_q_len < 1 || max_seq_len < 0 || num_splits < 0)
     return PKV_ERR_INVALID;
   if (max_q_len > kMultiMaxQ) return PKV_ERR_UNSUPPORTED;
   const MultiPlan m = make_multi_plan(batch, total_q, num_q_heads, num_kv_heads, max_q_len,
-                                      max_seq_len, num_splits);
+                                      max_seq_len, num_splits, dtype);
   if (splits_out) *splits_out = m.p.splits;
   if (pages_per_split_out) *pages_per_split_out = m.p.pages_per_split;
   if (workspace_bytes_out) *workspace_bytes_out = m.p.ws_bytes;
   return PKV_OK;
+}
+
+pkv_status pkv_decode_multi_plan(int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t max_q_len, int32_t max_seq_len,
+                                 int32_t num_splits, int32_t* splits_out,
+                                 int32_t* pages_per_split_out, size_t* workspace_bytes_out) {
+  return multi_plan_call(batch, total_q, num_q_heads, num_kv_heads, max_q_len, max_seq_len,
+                         num_splits, PKV_BF16, splits_out, pages_per_split_out,
+                         workspace_bytes_out);
+}
+
+pkv_status pkv_decode_multi_int4_plan(int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t max_q_len,
+                                      int32_t max_seq_len, int32_t num_splits,
+                                      int32_t* splits_out, int32_t* pages_per_split_out,
+                                      size_t* workspace_bytes_out) {
+  return multi_plan_call(batch, total_q, num_q_heads, num_kv_heads, max_q_len, max_seq_len,
+                         num_splits, PKV_INT4, splits_out, pages_per_split_out,
+                         workspace_bytes_out);
 }
 
 static pkv_status multi_call(const pkv_pool* pool, int32_t dtype, const void* q, int32_t total_q,
@@ -595,7 +645,7 @@ static pkv_status multi_call(const pkv_pool* pool, int32_t dtype, const void* q,
     if (st != PKV_OK) return st;
   }
   const MultiPlan m = make_multi_plan(batch, total_q, num_q_heads, pool->num_kv_heads, max_q_len,
-                                      max_seq_len, num_splits);
+                                      max_seq_len, num_splits, dtype);
   if (m.p.ws_bytes > 0 &&
       (!workspace || workspace_bytes < m.p.ws_bytes || !aligned(workspace, 256)))
     return PKV_ERR_INVALID;

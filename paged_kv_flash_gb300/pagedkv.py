@@ -62,6 +62,8 @@ SIGNATURES = {
                                    ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
     "pkv_paged_attn_decode_multi": (_I, [_POOLP, _P, _I, _P, _I, _I, _P, _I, _P, _I, _I, _F, _I,
                                          _P, _SZ, _P, _P, _P]),
+    "pkv_decode_multi_int4_plan": (_I, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_I),
+                                        ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
     "pkv_paged_attn_decode_multi_int4": (_I, [_POOLP, _P, _I, _P, _I, _I, _P, _I, _P, _I, _I, _F,
                                               _P, _I, _P, _SZ, _P, _P, _P]),
     "pkv_qkv_norm_rope_append": (_I, [_POOLP, _P, _I, _I, _P, _P, _F, _P, _P, _I, _P, _I, _P,
@@ -91,14 +93,21 @@ def lib_path() -> str:
     return _LIB_PATH
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+# The current stream's handle without building a Stream object (3 us a call,
+# a fifth of a small decode's host time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(status: int, what: str):
@@ -154,15 +163,14 @@ class Pool:
         """The C struct of the pool, rebuilt (and the tensors checked) only
         when a tensor has changed (it is passed on every call, and a serving
         loop makes many)."""
-        key = (self.k.data_ptr(), self.v.data_ptr(),
-               self.k_scale.data_ptr() if self.k_scale is not None else None,
-               self.v_scale.data_ptr() if self.v_scale is not None else None,
-               tuple(self.k.shape), tuple(self.v.shape), self.k.device, self.dtype)
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        key = (k.data_ptr(), v.data_ptr(), ks is not None and ks.data_ptr(),
+               vs is not None and vs.data_ptr(), k.shape, v.shape, k.dtype, k.device)
         cached = self.__dict__.get("_c")
         if cached is None or cached[0] != key:
             self._validate()
-            cached = (key, _Pool(key[0], key[1], key[2], key[3], *key[4][:2], PAGE_SIZE, HEAD_DIM,
-                                 key[7]))
+            cached = (key, _Pool(key[0], key[1], key[2] or None, key[3] or None, *key[4][:2],
+                                 PAGE_SIZE, HEAD_DIM, self.dtype))
             self.__dict__["_c"] = cached
         return cached[1]
 
@@ -430,13 +438,14 @@ def overlap_prefill_ctas(prefill_flops, decode_bytes):
 
 
 def decode_multi_plan(batch, total_q, num_q_heads, num_kv_heads, max_q_len, max_seq_len,
-                      num_splits=0):
-    """(splits, pages_per_split, workspace_bytes) of a multi-token decode."""
+                      num_splits=0, dtype=BF16):
+    """(splits, pages_per_split, workspace_bytes) of a multi-token decode on a
+    pool of the given dtype (BF16 or INT4)."""
     s, c, w = _I(), _I(), _SZ()
-    st = _lib.pkv_decode_multi_plan(batch, total_q, num_q_heads, num_kv_heads, max_q_len,
-                                    max_seq_len, num_splits, ctypes.byref(s), ctypes.byref(c),
-                                    ctypes.byref(w))
-    _check(st, "pkv_decode_multi_plan")
+    name = "pkv_decode_multi_int4_plan" if dtype == INT4 else "pkv_decode_multi_plan"
+    st = getattr(_lib, name)(batch, total_q, num_q_heads, num_kv_heads, max_q_len, max_seq_len,
+                             num_splits, ctypes.byref(s), ctypes.byref(c), ctypes.byref(w))
+    _check(st, name)
     return s.value, c.value, w.value
 
 
@@ -454,7 +463,7 @@ def paged_attn_decode_multi(pool: Pool, q, cu_q, block_table, seq_lens, max_q_le
     B = seq_lens.shape[0]
     if workspace is None:
         _, _, wsb = decode_multi_plan(B, T, Hq, pool.num_kv_heads, int(max_q_len),
-                                      int(max_seq_len), num_splits)
+                                      int(max_seq_len), num_splits, pool.dtype)
         workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=q.device)
     if out is None:
         out = torch.empty_like(q)
