@@ -7,6 +7,8 @@
 // (INT8) and writes 2 x 4,096.  One warp per (sequence, page, KV head): 16
 // lanes hold a row's 128 channels, 8 each, so every store instruction writes
 // two whole 256-byte rows, and all loads of a slab go out before its stores.
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -77,38 +79,43 @@ template <bool INT4>
 __global__ void __launch_bounds__(kWarps * 32)
     unpack_kernel(const __grid_constant__ pkv_host::UnpackLaunch a) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);      // (page, head) of the sequence
-  const int lp = unit / a.num_kv_heads, h = unit % a.num_kv_heads;
   const int L = __ldg(a.seq_lens + b);
   const int start = a.starts ? __ldg(a.starts + b) : 0;
   if (L < 0 || L > a.max_seq_len || start < 0) {
-    if (unit == 0 && lane == 0) atomicOr(&g_err_unpack, kErrBadIndex);
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_err_unpack, kErrBadIndex);
     return;
   }
-  const int lo = start - lp * kPageSize, hi = min(kPageSize, L - lp * kPageSize);
-  if (hi <= 0 || lo >= hi) return;
-  const int ps = __ldg(a.src_table + (size_t)b * a.src_max_pages + lp);
-  const int pd = __ldg(a.dst_table + (size_t)b * a.dst_max_pages + lp);
-  if (ps < 0 || ps >= a.src_pages || pd < 0 || pd >= a.dst_pages) {
-    if (lane == 0) atomicOr(&g_err_unpack, kErrBadIndex);
-    return;
-  }
-  const size_t slab = (size_t)ps * a.num_kv_heads + h;
-  const size_t out = ((size_t)pd * a.num_kv_heads + h) * kPageSize * (kHeadDim / 8);   // 16-byte units
+  if (start >= L) return;
   float w[8];
   if (a.k_smooth) {
     const float4* ws = reinterpret_cast<const float4*>(a.k_smooth) + 2 * (lane & 15);
     const float4 w0 = __ldg(ws), w1 = __ldg(ws + 1);
     w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w;
     w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
-    unpack_slab<INT4, true>(a.k, a.k_scale, slab, static_cast<uint4*>(a.k_out) + out, lo, hi, w,
-                            lane);
-  } else {
-    unpack_slab<INT4, false>(a.k, a.k_scale, slab, static_cast<uint4*>(a.k_out) + out, lo, hi, w,
+  }
+  // (page, head) pairs of the sequence's range, over the warps of its CTAs
+  const int first = start / kPageSize, pages = (L + kPageSize - 1) / kPageSize - first;
+  const long long units = (long long)pages * a.num_kv_heads;
+  for (long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < units;
+       unit += (long long)gridDim.x * kWarps) {
+    const int lp = first + (int)(unit / a.num_kv_heads), h = (int)(unit % a.num_kv_heads);
+    const int lo = start - lp * kPageSize, hi = min(kPageSize, L - lp * kPageSize);
+    const int ps = __ldg(a.src_table + (size_t)b * a.src_max_pages + lp);
+    const int pd = __ldg(a.dst_table + (size_t)b * a.dst_max_pages + lp);
+    if (ps < 0 || ps >= a.src_pages || pd < 0 || pd >= a.dst_pages) {
+      if (lane == 0) atomicOr(&g_err_unpack, kErrBadIndex);
+      continue;
+    }
+    const size_t slab = (size_t)ps * a.num_kv_heads + h;
+    const size_t out = ((size_t)pd * a.num_kv_heads + h) * (kPageSize * kHeadDim / 8);   // 16-byte units
+    uint4* k_out = static_cast<uint4*>(a.k_out) + out;
+    if (a.k_smooth)
+      unpack_slab<INT4, true>(a.k, a.k_scale, slab, k_out, lo, hi, w, lane);
+    else
+      unpack_slab<INT4, false>(a.k, a.k_scale, slab, k_out, lo, hi, w, lane);
+    unpack_slab<INT4, false>(a.v, a.v_scale, slab, static_cast<uint4*>(a.v_out) + out, lo, hi, w,
                              lane);
   }
-  unpack_slab<INT4, false>(a.v, a.v_scale, slab, static_cast<uint4*>(a.v_out) + out, lo, hi, w,
-                           lane);
 }
 
 }  // namespace
@@ -116,9 +123,13 @@ __global__ void __launch_bounds__(kWarps * 32)
 namespace pkv_host {
 
 cudaError_t launch_unpack(const UnpackLaunch& a, bool int4, cudaStream_t s) {
+  // Enough CTAs for the longest sequence, at most 16 per SM in all: each walks
+  // the sequence's own range, so that short ranges behind long prefixes (an
+  // append's new positions) do not cost a CTA per page of max_seq_len.
   const long long units =
       (long long)((a.max_seq_len + kPageSize - 1) / kPageSize) * a.num_kv_heads;
-  const long long blocks = (units + kWarps - 1) / kWarps;
+  const long long blocks = std::max<long long>(
+      1, std::min<long long>((units + kWarps - 1) / kWarps, 16ll * sm_count() / a.batch));
   const dim3 grid((unsigned)blocks, a.batch);
   if (int4)
     unpack_kernel<true><<<grid, kWarps * 32, 0, s>>>(a);

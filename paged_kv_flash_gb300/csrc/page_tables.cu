@@ -3,14 +3,13 @@
 // kernels, FlashAttention and PagedAttention": the block table that maps
 // positions to pages), with the free pages in a ring.
 //
-// Two launches.  The plan kernel, one CTA, sums tokens and pages over the
-// requests (first the totals, so that a step that does not fit is refused
-// before anything is written, then the prefix sums) and writes the new
-// lengths and the ring's new state; being one CTA, it may write them over its
-// inputs.  The fill kernel, the whole GPU, works from those outputs alone (the
-// old lengths and the old ends of the ring follow from the new ones and the
-// sums), one thread per new token, per page taken and per page freed, each of
-// which finds its request by binary search in a prefix sum.
+// One CTA (the plan) counts tokens and pages of the requests, scans them and
+// writes the prefix sums, the new lengths and the ring's new state; being one
+// CTA, it may write them over its inputs.  What follows from them -- a slot per
+// new token, an entry per page taken, a ring place per page freed -- the same
+// CTA writes when it is little (a decode step: one launch), the whole GPU in a
+// second launch otherwise, from the plan's outputs alone (the old lengths and
+// the old ends of the ring follow from the new ones and the sums).
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,82 +21,108 @@ using namespace pkv;
 
 __device__ uint32_t g_err_tables;
 
-constexpr int kPlanThreads = 1024;
+constexpr int kThreads = 1024;                      // of the plan CTA
+constexpr int kItems = 4;                           // requests per thread of a tile
+constexpr int kTile = kThreads * kItems;
 constexpr int kFillThreads = 256;
+constexpr int kChunk = 512;                         // tokens a warp of the fill takes at a time
+// The plan CTA fills in what follows for at most this many requests (their sums
+// and lengths in shared memory), tokens and pages that could be freed.
+constexpr int kAloneBatch = 2048, kAloneTokens = 8192, kAlonePages = 131072;
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kPageSize - 1) / kPageSize; }
 
-// Last b with cu[b] <= t (cu written by an earlier kernel of the step).
-__device__ __forceinline__ int find_owner(const int32_t* cu, int batch, int t) {
-  int lo = 0, hi = batch;
+// Last b in [lo, hi) with cu[b] <= t, given that cu[lo] <= t.
+__device__ __forceinline__ int find_owner(const int32_t* cu, int lo, int hi, int t) {
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = lo + ((hi - lo) >> 1);
     if (cu[mid] <= t) lo = mid; else hi = mid;
   }
   return lo;
 }
 
-struct Counts {
-  int tokens, taken, freed;
-};
-
-__device__ __forceinline__ Counts counts_of(int len, int fresh) {
-  Counts c{0, 0, 0};
-  if (fresh < 0) {
-    c.freed = pages_of(len);
-  } else {
-    c.tokens = fresh;
-    c.taken = pages_of(len + fresh) - pages_of(len);
-  }
-  return c;
+__device__ __forceinline__ int checked(const pkv_host::TablesLaunch& a, int page) {
+  if (page < 0 || page >= a.num_pages) atomicOr(&g_err_tables, kErrBadIndex);
+  return page;
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
-    plan_kernel(const __grid_constant__ pkv_host::TablesLaunch a) {
+__device__ __forceinline__ int ring_at(const pkv_host::TablesLaunch& a, int head, int i) {
+  long long at = (long long)head + i;                // both below the capacity
+  return (int)(at >= a.ring_capacity ? at - a.ring_capacity : at);
+}
+
+// The slot of position p of request b, which had `len` positions and takes its
+// pages from ring place `from` (counted from the ring's head).
+__device__ __forceinline__ int slot_of(const pkv_host::TablesLaunch& a, int b, int len, int head,
+                                       int from, int p) {
+  const int lp = p / kPageSize, held = pages_of(len);
+  const int page = checked(a, lp < held ? a.table[(size_t)b * a.max_pages + lp]
+                                        : a.ring[ring_at(a, head, from + lp - held)]);
+  return page >= 0 && page < a.num_pages ? page * kPageSize + p % kPageSize : -1;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    plan_kernel(const __grid_constant__ pkv_host::TablesLaunch a, const bool alone) {
   pdl_trigger();                                   // the fill kernel may be placed now
   constexpr uint32_t FULL = 0xffffffffu;
   __shared__ long long total[3];
-  __shared__ int bad;
-  __shared__ int wsum[3][32], carry[3];
+  __shared__ int bad, wsum[3][32], carry[3];
+  __shared__ int32_t s_cu[3][kAloneBatch + 1], s_len[kAloneBatch];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    bad = 0;
-    total[0] = total[1] = total[2] = 0;
+  if (tid < 3) {
+    total[tid] = 0;
+    carry[tid] = 0;
   }
-  if (tid < 3) carry[tid] = 0;
+  if (tid == 3) bad = 0;
+  const int head = a.ring_state[0], count = a.ring_state[1];
+  const int most = a.max_pages * kPageSize, cap = a.ring_capacity;
   __syncthreads();
 
-  // totals and checks
-  const int most = a.max_pages * kPageSize;
-  long long sum[3] = {0, 0, 0};
-  bool wrong = false;
-  for (long long b = tid; b < a.batch; b += kPlanThreads) {
-    const int len = a.seq_lens[b], fresh = a.new_lens[b];
-    if (len < 0 || len > most || (long long)len + fresh > most) {
-      wrong = true;
-      continue;
-    }
-    const Counts c = counts_of(len, fresh);
-    sum[0] += c.tokens;
-    sum[1] += c.taken;
-    sum[2] += c.freed;
-  }
+  // A tile's lengths and counts (tokens, pages taken, pages freed); false if a
+  // length is not one.
+  int len[kItems], n[3][kItems];
+  auto load = [&](long long base) {
+    bool ok = true;
 #pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    for (int x = 16; x >= 1; x >>= 1) sum[j] += __shfl_xor_sync(FULL, sum[j], x);
-    if (lane == 0 && sum[j]) atomicAdd(reinterpret_cast<unsigned long long*>(&total[j]),
-                                       (unsigned long long)sum[j]);
+    for (int i = 0; i < kItems; ++i) {
+      const long long b = base + (long long)tid * kItems + i;
+      const bool on = b < a.batch;
+      len[i] = on ? a.seq_lens[b] : 0;
+      const int fresh = on ? a.new_lens[b] : 0;
+      n[0][i] = n[1][i] = n[2][i] = 0;
+      if (len[i] < 0 || len[i] > most || (long long)len[i] + fresh > most) {
+        ok = false;
+      } else if (fresh < 0) {
+        n[2][i] = pages_of(len[i]);
+        if (on) len[i] = -1 - len[i];               // ended: marked by its sign
+      } else {
+        n[0][i] = fresh;
+        n[1][i] = pages_of(len[i] + fresh) - pages_of(len[i]);
+      }
+    }
+    return ok;
+  };
+  // totals and checks first: a step that does not fit writes nothing
+  for (long long base = 0; base < a.batch; base += kTile) {
+    if (!load(base)) bad = 1;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      long long sum = 0;
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) sum += n[q][i];
+#pragma unroll
+      for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
+      if (lane == 0 && sum)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&total[q]), (unsigned long long)sum);
+    }
   }
-  if (wrong) bad = 1;
-  const int head = a.ring_state[0], count = a.ring_state[1];
   __syncthreads();
-  const int cap = a.ring_capacity;
   const bool refuse =
       bad || head < 0 || head >= cap || count < 0 || count > cap || total[1] > count ||
-      (long long)count - total[1] + total[2] > cap || total[0] > 2147483647ll ||
+      count + total[2] > cap || total[0] > 2147483647ll ||
       (a.slots && total[0] > a.slot_capacity);
   if (refuse) {
-    for (long long b = tid; b <= a.batch; b += kPlanThreads) {
+    for (long long b = tid; b <= a.batch; b += kThreads) {
       a.cu_new[b] = a.taken[b] = a.freed[b] = 0;
       if (b < a.batch) a.seq_lens_out[b] = a.seq_lens[b];
     }
@@ -109,22 +134,27 @@ __global__ void __launch_bounds__(kPlanThreads)
     return;
   }
 
-  // prefix sums, 1,024 requests at a time
-  for (long long base = 0; base < a.batch; base += kPlanThreads) {
-    const long long b = base + tid;
-    const bool on = b < a.batch;
-    const int len = on ? a.seq_lens[b] : 0, fresh = on ? a.new_lens[b] : 0;
-    const Counts c = counts_of(len, fresh);
-    int v[3] = {c.tokens, c.taken, c.freed};
+  // prefix sums, a tile at a time (the only tile's counts are still here)
+  int32_t* const out[3] = {a.cu_new, a.taken, a.freed};
+  for (long long base = 0; base < a.batch; base += kTile) {
+    if (a.batch > kTile) load(base);
+    int v[3];
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
+    for (int q = 0; q < 3; ++q) {
 #pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const int up = __shfl_up_sync(FULL, v[j], x);
-        if (lane >= x) v[j] += up;
-      }
-      if (lane == 31) wsum[j][warp] = v[j];
+      for (int i = 1; i < kItems; ++i) n[q][i] += n[q][i - 1];
+      v[q] = n[q][kItems - 1];
     }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const int up = __shfl_up_sync(FULL, v[q], x);
+        if (lane >= x) v[q] += up;
+      }
+    if (lane == 31)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) wsum[q][warp] = v[q];
     __syncthreads();
     if (warp < 3) {
       int w = wsum[warp][lane];
@@ -136,12 +166,26 @@ __global__ void __launch_bounds__(kPlanThreads)
       wsum[warp][lane] = w;
     }
     __syncthreads();
-    if (on) {
-      int32_t* out[3] = {a.cu_new, a.taken, a.freed};
 #pragma unroll
-      for (int j = 0; j < 3; ++j)
-        out[j][b + 1] = carry[j] + v[j] + (warp ? wsum[j][warp - 1] : 0);
-      a.seq_lens_out[b] = fresh < 0 ? 0 : len + fresh;
+    for (int q = 0; q < 3; ++q) {
+      const int before = carry[q] + (warp ? wsum[q][warp - 1] : 0) + v[q] - n[q][kItems - 1];
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const long long b = base + (long long)tid * kItems + i;
+        if (b < a.batch) {
+          out[q][b + 1] = before + n[q][i];
+          if (alone) s_cu[q][b + 1] = before + n[q][i];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const long long b = base + (long long)tid * kItems + i;
+      if (b < a.batch) {
+        const int fresh = n[0][i] - (i ? n[0][i - 1] : 0);
+        a.seq_lens_out[b] = len[i] < 0 ? 0 : len[i] + fresh;
+        if (alone) s_len[b] = len[i] < 0 ? -1 - len[i] : len[i];
+      }
     }
     __syncthreads();
     if (tid < 3) carry[tid] += wsum[tid][31];
@@ -149,44 +193,90 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   if (tid == 0) {
     a.cu_new[0] = a.taken[0] = a.freed[0] = 0;
+    s_cu[0][0] = s_cu[1][0] = s_cu[2][0] = 0;
     a.ring_state_out[0] = (int)(((long long)head + total[1]) % cap);
     a.ring_state_out[1] = (int)(count - total[1] + total[2]);
   }
+  if (!alone) return;
+  __syncthreads();
+
+  // the rest of a small step
+  const int B = a.batch;
+  if (a.slots)
+    for (int t = tid; t < (int)total[0]; t += kThreads) {
+      const int b = find_owner(s_cu[0], 0, B, t);
+      a.slots[t] = slot_of(a, b, s_len[b], head, s_cu[1][b], s_len[b] + (t - s_cu[0][b]));
+    }
+  for (int i = tid; i < (int)total[1]; i += kThreads) {
+    const int b = find_owner(s_cu[1], 0, B, i);
+    a.table[(size_t)b * a.max_pages + pages_of(s_len[b]) + (i - s_cu[1][b])] =
+        checked(a, a.ring[ring_at(a, head, i)]);
+  }
+  const int tail = ring_at(a, head, count) % cap;
+  for (int i = tid; i < (int)total[2]; i += kThreads) {
+    const int b = find_owner(s_cu[2], 0, B, i);
+    a.ring[ring_at(a, tail, i)] = checked(a, a.table[(size_t)b * a.max_pages + (i - s_cu[2][b])]);
+  }
 }
 
+// The same for a large step, on the whole GPU.  A warp takes 512 consecutive
+// tokens: two binary searches in global memory bound the requests they belong
+// to, so that the search of each token is over those alone (none where a prompt
+// holds them all), and four tokens a lane make a 16-byte store.
 __global__ void __launch_bounds__(kFillThreads)
     fill_kernel(const __grid_constant__ pkv_host::TablesLaunch a) {
   pdl_wait();                                      // the plan's outputs
   const int B = a.batch, cap = a.ring_capacity;
   const int tokens = a.slots ? a.cu_new[B] : 0, taken = a.taken[B], freed = a.freed[B];
   const int head_new = a.ring_state_out[0], count_new = a.ring_state_out[1];
-  const int head = (int)((((long long)head_new - taken) % cap + cap) % cap);   // before the step
-  const int tail = (int)((((long long)head_new + count_new - freed) % cap + cap) % cap);
-  const long long work = (long long)tokens + taken + freed;
-  for (long long i = (long long)blockIdx.x * kFillThreads + threadIdx.x; i < work;
-       i += (long long)gridDim.x * kFillThreads) {
-    if (i < tokens) {
-      const int t = (int)i, b = find_owner(a.cu_new, B, t);
-      const int first = a.cu_new[b];
-      const int len = a.seq_lens_out[b] - (a.cu_new[b + 1] - first);    // before the step
-      const int p = len + (t - first), lp = p / kPageSize, held = pages_of(len);
-      const int page = lp < held
-                           ? a.table[(size_t)b * a.max_pages + lp]
-                           : a.ring[((long long)head + a.taken[b] + (lp - held)) % cap];
-      const bool ok = page >= 0 && page < a.num_pages;
-      if (!ok) atomicOr(&g_err_tables, kErrBadIndex);
-      a.slots[t] = ok ? page * kPageSize + p % kPageSize : -1;
-    } else if (i < (long long)tokens + taken) {
-      const int j = (int)(i - tokens), b = find_owner(a.taken, B, j);
+  const int head = (int)(((long long)head_new - taken + cap) % cap);            // before the step
+  const int tail = (int)(((long long)head_new + count_new - freed + cap) % cap);
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * (kFillThreads / 32);
+  const long long me = (long long)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5);
+  const bool wide = (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
+  for (long long base = me * kChunk; base < tokens; base += warps * kChunk) {
+    const int end = (int)min((long long)tokens, base + kChunk);
+    const int b0 = find_owner(a.cu_new, 0, B, (int)base);
+    const int b1 = find_owner(a.cu_new, b0, B, end - 1) + 1;
+    for (int t0 = (int)base + 4 * lane; t0 < end; t0 += 128) {
+      int b = find_owner(a.cu_new, b0, b1, t0);
+      int first = a.cu_new[b], next = a.cu_new[b + 1];
+      int slot[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = t0 + e;
+        slot[e] = -1;
+        if (t >= end) continue;
+        if (t >= next) {
+          b = find_owner(a.cu_new, b + 1, b1, t);
+          first = a.cu_new[b];
+          next = a.cu_new[b + 1];
+        }
+        const int len = a.seq_lens_out[b] - (next - first);                     // before the step
+        slot[e] = slot_of(a, b, len, head, a.taken[b], len + (t - first));
+      }
+      if (wide && t0 + 4 <= end) {
+        *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t0 + e < end) a.slots[t0 + e] = slot[e];
+      }
+    }
+  }
+  const long long threads = (long long)gridDim.x * kFillThreads;
+  for (long long i = (long long)blockIdx.x * kFillThreads + threadIdx.x;
+       i < (long long)taken + freed; i += threads) {
+    if (i < taken) {
+      const int j = (int)i, b = find_owner(a.taken, 0, B, j);
       const int len = a.seq_lens_out[b] - (a.cu_new[b + 1] - a.cu_new[b]);
-      const int page = a.ring[((long long)head + j) % cap];
-      if (page < 0 || page >= a.num_pages) atomicOr(&g_err_tables, kErrBadIndex);
-      a.table[(size_t)b * a.max_pages + pages_of(len) + (j - a.taken[b])] = page;
+      a.table[(size_t)b * a.max_pages + pages_of(len) + (j - a.taken[b])] =
+          checked(a, a.ring[ring_at(a, head, j)]);
     } else {
-      const int j = (int)(i - tokens - taken), b = find_owner(a.freed, B, j);
-      const int page = a.table[(size_t)b * a.max_pages + (j - a.freed[b])];
-      if (page < 0 || page >= a.num_pages) atomicOr(&g_err_tables, kErrBadIndex);
-      a.ring[((long long)tail + j) % cap] = page;
+      const int j = (int)(i - taken), b = find_owner(a.freed, 0, B, j);
+      a.ring[ring_at(a, tail, j)] =
+          checked(a, a.table[(size_t)b * a.max_pages + (j - a.freed[b])]);
     }
   }
 }
@@ -196,12 +286,16 @@ __global__ void __launch_bounds__(kFillThreads)
 namespace pkv_host {
 
 cudaError_t launch_tables(const TablesLaunch& a, cudaStream_t s) {
-  plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // one thread per token and page as far as the host knows them (the slot
-  // map's size and four pages per request), at most eight CTAs per SM
-  const long long guess = (long long)a.slot_capacity + 4ll * a.batch;
+  const long long could_free =
+      std::min<long long>((long long)a.batch * a.max_pages, a.ring_capacity);
+  const bool alone =
+      a.batch <= kAloneBatch && a.slot_capacity <= kAloneTokens && could_free <= kAlonePages;
+  plan_kernel<<<1, kThreads, 0, s>>>(a, alone);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || alone) return e;
+  // a warp per 512 tokens and a thread per page, as far as the host knows them
+  // (the slot map's size, four pages a request), at most eight CTAs per SM
+  const long long guess = a.slot_capacity / (kChunk / 32) + 4ll * a.batch;
   const int grid = (int)std::max<long long>(
       1, std::min<long long>((guess + kFillThreads - 1) / kFillThreads, 8ll * sm_count()));
   return launch_dependent(fill_kernel, dim3(grid), dim3(kFillThreads), s, a);

@@ -106,6 +106,30 @@ def test_steps_match_the_host(pk, B, in_place):
         eq(d["ring_state"], [host.head, host.count])
 
 
+@pytest.mark.parametrize("B,choices", [(2000, [-1, 0, 1, 2]), (2049, [0, 1]), (3, [2700]),
+                                       (3, [2800, 0]), (900, [-1])])
+def test_small_and_large_steps(pk, B, choices):
+    """Either side of what one CTA does alone: many requests of few tokens, few
+    of many, all of them ending."""
+    rng = np.random.default_rng(1050 + B)
+    host = Host(rng, rng.integers(0, 60, B), max_pages=400, spare=B * 3 + 1200)
+    d = host.device()
+    for _ in range(2):
+        new = rng.choice(choices, B)
+        tokens = int(np.maximum(new, 0).sum())
+        slots = torch.full((tokens + 1,), -9, dtype=torch.int32, device="cuda")[1:]    # unaligned
+        offs = torch.empty((2, B + 1), dtype=torch.int32, device="cuda")
+        cu, lens = pk.page_tables(d["seq_lens"], dev(new.astype(np.int32)), d["block_table"],
+                                  d["free_ring"], d["ring_state"], host.num_pages,
+                                  slot_map=slots if tokens else None, page_offsets=offs)
+        assert pk.poll_device_error() == pk.OK
+        hcu, hoffs, hslots = host.step(new)
+        for got, want in ((cu, hcu), (offs, hoffs), (slots, hslots), (lens, host.lens),
+                          (d["block_table"], host.table), (d["free_ring"], host.ring),
+                          (d["ring_state"], [host.head, host.count])):
+            eq(got, want)
+
+
 def test_the_last_free_page_and_no_slot_map(pk):
     """Exactly as many pages as are free; no slot map; a request of no tokens."""
     rng = np.random.default_rng(1100)
