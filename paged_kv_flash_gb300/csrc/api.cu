@@ -112,13 +112,12 @@ struct Plan {
 // splits of the most pages takes longer ones still where those make a single
 // wave (eight 32k-position sequences: 9 splits of 232 pages 66.8 us, 16 of 128
 // 68.6 us, 12 of 176, a wave and a quarter, 76.8 us).
-constexpr int kInt4CtasPerSm = 4, kInt4Round = 8, kInt4WaveMaxPages = 256;
-constexpr int kInt4MultiMinPages = 16;
+constexpr int kInt4Round = 8, kInt4WaveMaxPages = 256;
 
 // Pages per split with which `units` work items of mp pages make one wave of
 // int4 CTAs.
 int int4_wave_pages(long long units, int mp) {
-  const long long s1 = std::max<long long>(1, (long long)sm_count() * kInt4CtasPerSm / units);
+  const long long s1 = std::max<long long>(1, (long long)sm_count() * pkv_host::kInt4CtasPerSm / units);
   const long long c = (mp + s1 - 1) / s1;
   return (int)((c + kInt4Round - 1) / kInt4Round * kInt4Round);
 }
@@ -141,8 +140,8 @@ Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, in
     const int round = dtype == PKV_INT4 ? kInt4Round : pkv_host::kDecodeWarps;
     c = (c + round - 1) / round * round;
     if (dtype == PKV_INT4 && c >= kPlanMaxPages) {
-      const int rows = num_q_heads / num_kv_heads;      // 8 of them a CTA
-      const int wave = int4_wave_pages((long long)batch * num_kv_heads * ((rows + 7) / 8), mp);
+      const int wave = int4_wave_pages(
+          pkv_host::int4_units(batch, num_kv_heads, num_q_heads / num_kv_heads), mp);
       if (wave <= kInt4WaveMaxPages) c = std::max<long long>(c, wave);
     }
     C = (int)std::min<long long>(c, mp);
@@ -200,9 +199,9 @@ struct MultiPlan {
   int row_groups;
 };
 
-// INT4 pools: one CTA per 8 rows, splits of 16..128 pages that make one wave
-// (a 16-token step at 1,024 positions: 4 splits of 16 pages 11.5 us, 8 of 8
-// 12.3 us; eight ragged steps at 4k..8k: 4 splits of 128 pages 85.8 us, 8 of 64
+// INT4 pools: one CTA per 8 rows, splits of 8..128 pages that make one wave
+// (a 16-token step at 1,024 positions: 8 splits of 8 pages 10.7 us, 4 of 16
+// 11.2 us; eight ragged steps at 4k..8k: 4 splits of 128 pages 85.8 us, 8 of 64
 // 94.2 us).
 MultiPlan make_multi_plan(int batch, int total_q, int num_q_heads, int num_kv_heads, int max_q,
                           int max_seq_len, int num_splits, int dtype) {
@@ -218,9 +217,8 @@ MultiPlan make_multi_plan(int batch, int total_q, int num_q_heads, int num_kv_he
     C = (mp + num_splits - 1) / num_splits;
   } else if (dtype == PKV_INT4) {
     const long long units =
-        std::max<long long>(1, (long long)batch * num_kv_heads * ((rows + 7) / 8));
-    C = std::min(mp, std::max(kInt4MultiMinPages,
-                              std::min((int)kPlanMaxPages, int4_wave_pages(units, mp))));
+        std::max<long long>(1, pkv_host::int4_units(batch, num_kv_heads, rows));
+    C = std::min(mp, std::min((int)kPlanMaxPages, int4_wave_pages(units, mp)));
   } else {
     const long long slots = (long long)sm_count() * kMultiCtasPerSm;
     const long long target = std::max<long long>(1, slots * kPlanSlotsNum / kPlanSlotsDen);

@@ -945,6 +945,10 @@ cudaError_t launch_decode(const DecodeLaunch& a, int dtype, cudaStream_t s) {
                   : dtype == PKV_INT8 ? dispatch_i8mma(a, s)
                                       : dispatch_group(a, s);
   if (e != cudaSuccess || a.splits == 1 || a.ws_ctr) return e;
+  if (dtype == PKV_INT4 &&
+      int4_merges_itself(a.splits, int4_units(a.batch, a.num_kv_heads,
+                                              a.num_q_heads / a.num_kv_heads)))
+    return e;
   // the combine's CTAs are placed while the split kernel's last ones run and
   // wait on the device for its partials, instead of a launch after it
   return launch_dependent(decode_combine_kernel, dim3(a.batch * a.num_q_heads), dim3(128), s, a);

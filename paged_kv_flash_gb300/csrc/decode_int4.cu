@@ -50,7 +50,7 @@ using namespace pkv;
 __device__ uint32_t g_err_int4;
 
 constexpr int W = 4;                                // warps per CTA
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = pkv_host::kInt4CtasPerSm;
 constexpr int kRows = 8;                            // query rows of a CTA: one n-tile
 // A warp takes two pages at a time (the wait, the maximum's shuffles and the
 // votes are per step), from a ring of two such buffers; the sixteen warps of an
@@ -76,6 +76,17 @@ constexpr int qfrag_bytes(int low) { return 2048 * (low == kLowApart ? 2 : 1); }
 constexpr int smem_of(int low) { return 1024 + qfrag_bytes(low) + W * kWarpBytes; }
 static_assert(kCtasPerSm * (smem_of(kLowApart) + 1024) <= 228 * 1024, "resident CTAs");
 
+// Where all CTAs of a call are resident at once, up to this many splits of a
+// (sequence, KV head, row group) run as one thread-block cluster and merge
+// through distributed shared memory: no partials in global memory and no second
+// launch (one sequence of 1,024 positions: 7.2 -> 6.1 us).  In larger calls a
+// cluster would hold the places of its finished splits until the last one is
+// done (64 sequences of 512..8,192 positions: 86 -> 106 us).
+constexpr int kClusterSplits = pkv_host::kInt4ClusterSplits;
+constexpr int kMergeAt = 4608;                      // the split's result, behind warp 0's parked one
+static_assert(kMergeAt >= kRows * (kHeadDim + 2) * 4 &&
+                  kMergeAt + kRows * (kHeadDim + 1) * 4 <= kWarpBytes, "both fit warp 0's ring");
+
 struct Launch {
   const uint8_t* k;
   const uint8_t* v;
@@ -90,6 +101,7 @@ struct Launch {
   float softmax_scale;
   const float* k_smooth;
   int splits, pages_per_split, row_groups;
+  bool clustered;          // the splits merge themselves
   uint32_t* ws_ctr;        // fused merge, as DecodeLaunch
   float* ws_o;
   float* ws_lse;
@@ -131,6 +143,20 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
 
 __device__ __forceinline__ float2 halves(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+
+// A float at `addr` of this CTA's shared memory, in the CTA of that rank.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
@@ -628,8 +654,9 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   }
   __syncthreads();
 
-  // Merge the warps (log-sum-exp rule); write the bf16 output (one split) or
-  // the split's partial.
+  // Merge the warps (log-sum-exp rule); write the bf16 output (one split), the
+  // split's result for its cluster, or its partial.
+  float* res = reinterpret_cast<float*>(bufs + kMergeAt);     // O [8][128], lse2 [8]
   const int rows = min(kRows, R - row0);
   for (int i = threadIdx.x; i < rows * kHeadDim; i += W * 32) {
     const int n = i / kHeadDim, d = i % kHeadDim;
@@ -653,13 +680,45 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     if (direct) {
       a.out[bh * kHeadDim + d] = __float2bfloat16_rn(O);
       if (a.lse && d == 0) a.lse[bh] = lse2 * kLn2;
+    } else if (a.clustered) {
+      res[i] = O;
+      if (d == 0) res[kRows * kHeadDim + n] = lse2;
     } else {
       const size_t slot = bh * a.splits + split;
       a.ws_o[slot * kHeadDim + d] = O;
       if (d == 0) a.ws_lse[slot] = lse2;
     }
   }
-  if (direct || !a.ws_ctr) return;                  // separate combine kernel
+  if (direct) return;                               // alone, or the only split with keys
+  if (a.clustered) {
+    // The nv splits with keys (the others have left) share the rows out; splits
+    // are added in order, so the result does not depend on which CTA merges.
+    cluster_sync();
+    const uint32_t res_s = smem_u32(res);
+    for (int n = split; n < rows; n += nv) {
+      float lse[kClusterSplits], M = -INFINITY, sum = 0.f, O = 0.f;
+#pragma unroll
+      for (int c = 0; c < kClusterSplits; ++c) {
+        lse[c] = c < nv ? ld_cluster(res_s + (kRows * kHeadDim + n) * 4, c) : -INFINITY;
+        M = fmaxf(M, lse[c]);
+      }
+      if (M != -INFINITY)
+#pragma unroll
+        for (int c = 0; c < kClusterSplits; ++c)
+          if (c < nv) {
+            const float f = fast_exp2(lse[c] - M);
+            sum += f;
+            O += f * ld_cluster(res_s + (n * kHeadDim + threadIdx.x) * 4, c);
+          }
+      const int rho = row0 + n;
+      const size_t bh = (size_t)(q0 + rho / G) * Hq + h * G + rho % G;
+      a.out[bh * kHeadDim + threadIdx.x] = __float2bfloat16_rn(M != -INFINITY ? O / sum : 0.f);
+      if (a.lse && threadIdx.x == 0) a.lse[bh] = (M + fast_log2(sum)) * kLn2;
+    }
+    cluster_sync();                                 // nobody reads this CTA any more
+    return;
+  }
+  if (!a.ws_ctr) return;                            // separate combine kernel
 
   // Fused merge (decode): the part that completes the count of (b, KV head)
   // merges the nv splits of its rows and resets the count.
@@ -683,12 +742,12 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   float* red = wsm + 128;
   for (int rho = 0; rho < R; ++rho) {
     const size_t bh = (size_t)(q0 + rho / G) * Hq + h * G + rho % G;
-    const float2 res = merge_splits(a.ws_lse + bh * a.splits, a.ws_o + bh * a.splits * kHeadDim,
+    const float2 m = merge_splits(a.ws_lse + bh * a.splits, a.ws_o + bh * a.splits * kHeadDim,
                                     nv, wsm, red);
     const int d = threadIdx.x;
     if (d < kHeadDim) {
-      a.out[bh * kHeadDim + d] = __float2bfloat16_rn(res.x);
-      if (a.lse && d == 0) a.lse[bh] = res.y * kLn2;
+      a.out[bh * kHeadDim + d] = __float2bfloat16_rn(m.x);
+      if (a.lse && d == 0) a.lse[bh] = m.y * kLn2;
     }
   }
 }
@@ -699,13 +758,26 @@ cudaError_t launch_as(const Launch& a, int batch, cudaStream_t s) {
   cudaError_t e = pkv_host::set_max_dynamic_smem(
       reinterpret_cast<const void*>(decode_int4_kernel<LOW>), smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.splits, a.num_kv_heads * a.row_groups, batch);
-  decode_int4_kernel<LOW><<<grid, W * 32, smem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.splits, a.num_kv_heads * a.row_groups, batch);
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (a.clustered) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, decode_int4_kernel<LOW>, a);
 }
 
 cudaError_t launch_rows(Launch& a, int rows, int batch, cudaStream_t s) {
   a.row_groups = (rows + kRows - 1) / kRows;
+  a.clustered = pkv_host::int4_merges_itself(
+      a.splits, pkv_host::int4_units(batch, a.num_kv_heads, rows));
   if (!a.k_smooth) return launch_as<kPlain>(a, batch, s);
   return rows <= kRows / 2 ? launch_as<kLowBeside>(a, batch, s) : launch_as<kLowApart>(a, batch, s);
 }
@@ -713,6 +785,11 @@ cudaError_t launch_rows(Launch& a, int rows, int batch, cudaStream_t s) {
 }  // namespace
 
 namespace pkv_host {
+
+bool int4_merges_itself(int splits, long long units) {
+  return splits > 1 && splits <= kInt4ClusterSplits &&
+         units * splits <= (long long)sm_count() * kInt4CtasPerSm;
+}
 
 cudaError_t launch_split_int4(const DecodeLaunch& d, cudaStream_t s) {
   Launch a{};

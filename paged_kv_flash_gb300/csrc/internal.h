@@ -145,6 +145,14 @@ struct MultiLaunch {
 cudaError_t launch_decode_multi(const MultiLaunch& a, bool int4, cudaStream_t s);
 uint32_t take_multi_error(cudaStream_t s);
 
+// Whether the int4 kernel merges the splits of a call itself, so that no combine
+// follows: units (sequence, KV head, 8 query rows) of that many splits.
+constexpr int kInt4ClusterSplits = 8;    // the portable cluster size
+constexpr int kInt4CtasPerSm = 4;
+bool int4_merges_itself(int splits, long long units);
+inline long long int4_units(int batch, int num_kv_heads, long long rows) {
+  return (long long)batch * num_kv_heads * ((rows + 7) / 8);
+}
 // The split kernel of both on an int4 pool (decode_int4.cu); launch_decode and
 // launch_decode_multi add the combine.  workspace as theirs.
 cudaError_t launch_split_int4(const DecodeLaunch& a, cudaStream_t s);

@@ -25,7 +25,7 @@ constexpr int kThreads = 1024;                      // of the plan CTA
 constexpr int kItems = 4;                           // requests per thread of a tile
 constexpr int kTile = kThreads * kItems;
 constexpr int kFillThreads = 256;
-constexpr int kChunk = 512;                         // tokens a warp of the fill takes at a time
+constexpr int kChunk = 256, kPageChunk = 64;       // tokens, pages a warp of the fill takes at a time
 // The plan CTA fills in what follows for at most this many requests (their sums
 // and lengths in shared memory), tokens and pages that could be freed.
 constexpr int kAloneBatch = 2048, kAloneTokens = 8192, kAlonePages = 131072;
@@ -37,6 +37,19 @@ __device__ __forceinline__ int find_owner(const int32_t* cu, int lo, int hi, int
   while (hi - lo > 1) {
     const int mid = lo + ((hi - lo) >> 1);
     if (cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The same for all lanes of a warp at once, 32 ways a round: three loads deep
+// for 32,768 requests where the binary search is fifteen.
+__device__ __forceinline__ int find_owner_warp(const int32_t* cu, int lo, int hi, int t, int lane) {
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int at = lo + lane * step;
+    const uint32_t m = __ballot_sync(0xffffffffu, at < hi && cu[at] <= t);    // a prefix of lanes
+    lo += (31 - __clz(m)) * step;
+    hi = min(hi, lo + step);
   }
   return lo;
 }
@@ -62,7 +75,8 @@ __device__ __forceinline__ int slot_of(const pkv_host::TablesLaunch& a, int b, i
 }
 
 __global__ void __launch_bounds__(kThreads)
-    plan_kernel(const __grid_constant__ pkv_host::TablesLaunch a, const bool alone) {
+    plan_kernel(const __grid_constant__ pkv_host::TablesLaunch a, const bool alone,
+                const bool small) {
   pdl_trigger();                                   // the fill kernel may be placed now
   constexpr uint32_t FULL = 0xffffffffu;
   __shared__ long long total[3];
@@ -110,8 +124,12 @@ __global__ void __launch_bounds__(kThreads)
       long long sum = 0;
 #pragma unroll
       for (int i = 0; i < kItems; ++i) sum += n[q][i];
+      if (small) {                                  // no sum can pass 31 bits
+        sum = __reduce_add_sync(FULL, (int)sum);
+      } else {
 #pragma unroll
-      for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
+        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
+      }
       if (lane == 0 && sum)
         atomicAdd(reinterpret_cast<unsigned long long*>(&total[q]), (unsigned long long)sum);
     }
@@ -220,9 +238,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // The same for a large step, on the whole GPU.  A warp takes 512 consecutive
-// tokens: two binary searches in global memory bound the requests they belong
-// to, so that the search of each token is over those alone (none where a prompt
-// holds them all), and four tokens a lane make a 16-byte store.
+// tokens, or 128 pages taken or freed: two searches by the warp bound the
+// requests they belong to, so that each lane's own search is over those alone
+// (none where one request holds them all); four tokens a lane make a 16-byte
+// store.
 __global__ void __launch_bounds__(kFillThreads)
     fill_kernel(const __grid_constant__ pkv_host::TablesLaunch a) {
   pdl_wait();                                      // the plan's outputs
@@ -232,51 +251,58 @@ __global__ void __launch_bounds__(kFillThreads)
   const int head = (int)(((long long)head_new - taken + cap) % cap);            // before the step
   const int tail = (int)(((long long)head_new + count_new - freed + cap) % cap);
   const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * (kFillThreads / 32);
-  const long long me = (long long)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5);
+  const int warps = gridDim.x * (kFillThreads / 32);
   const bool wide = (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
-  for (long long base = me * kChunk; base < tokens; base += warps * kChunk) {
-    const int end = (int)min((long long)tokens, base + kChunk);
-    const int b0 = find_owner(a.cu_new, 0, B, (int)base);
-    const int b1 = find_owner(a.cu_new, b0, B, end - 1) + 1;
-    for (int t0 = (int)base + 4 * lane; t0 < end; t0 += 128) {
-      int b = find_owner(a.cu_new, b0, b1, t0);
-      int first = a.cu_new[b], next = a.cu_new[b + 1];
-      int slot[4];
+  const int c_tokens = (int)(((long long)tokens + kChunk - 1) / kChunk);
+  const int c_taken = (int)(((long long)taken + kPageChunk - 1) / kPageChunk);
+  const int c_freed = (int)(((long long)freed + kPageChunk - 1) / kPageChunk);
+  for (int c = blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5);
+       c < c_tokens + c_taken + c_freed; c += warps) {
+    const int kind = c < c_tokens ? 0 : (c < c_tokens + c_taken ? 1 : 2);
+    const int32_t* cu = kind == 0 ? a.cu_new : (kind == 1 ? a.taken : a.freed);
+    const int total = kind == 0 ? tokens : (kind == 1 ? taken : freed);
+    const int size = kind == 0 ? kChunk : kPageChunk;
+    const int base = (c - (kind == 0 ? 0 : (kind == 1 ? c_tokens : c_tokens + c_taken))) * size;
+    const int end = (int)min((long long)total, (long long)base + size);
+    const int b0 = find_owner_warp(cu, 0, B, base, lane);
+    const int b1 = find_owner_warp(cu, b0, B, end - 1, lane) + 1;
+    if (kind == 0) {
+      for (int t0 = base + 4 * lane; t0 < end; t0 += 128) {
+        int b = find_owner(cu, b0, b1, t0);
+        int first = cu[b], next = cu[b + 1];
+        int slot[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = t0 + e;
-        slot[e] = -1;
-        if (t >= end) continue;
-        if (t >= next) {
-          b = find_owner(a.cu_new, b + 1, b1, t);
-          first = a.cu_new[b];
-          next = a.cu_new[b + 1];
+        for (int e = 0; e < 4; ++e) {
+          const int t = t0 + e;
+          slot[e] = -1;
+          if (t >= end) continue;
+          if (t >= next) {
+            b = find_owner(cu, b + 1, b1, t);
+            first = cu[b];
+            next = cu[b + 1];
+          }
+          const int len = a.seq_lens_out[b] - (next - first);                   // before the step
+          slot[e] = slot_of(a, b, len, head, a.taken[b], len + (t - first));
         }
-        const int len = a.seq_lens_out[b] - (next - first);                     // before the step
-        slot[e] = slot_of(a, b, len, head, a.taken[b], len + (t - first));
-      }
-      if (wide && t0 + 4 <= end) {
-        *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      } else {
+        if (wide && t0 + 4 <= end) {
+          *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (t0 + e < end) a.slots[t0 + e] = slot[e];
+          for (int e = 0; e < 4; ++e)
+            if (t0 + e < end) a.slots[t0 + e] = slot[e];
+        }
       }
-    }
-  }
-  const long long threads = (long long)gridDim.x * kFillThreads;
-  for (long long i = (long long)blockIdx.x * kFillThreads + threadIdx.x;
-       i < (long long)taken + freed; i += threads) {
-    if (i < taken) {
-      const int j = (int)i, b = find_owner(a.taken, 0, B, j);
-      const int len = a.seq_lens_out[b] - (a.cu_new[b + 1] - a.cu_new[b]);
-      a.table[(size_t)b * a.max_pages + pages_of(len) + (j - a.taken[b])] =
-          checked(a, a.ring[ring_at(a, head, j)]);
     } else {
-      const int j = (int)(i - taken), b = find_owner(a.freed, 0, B, j);
-      a.ring[ring_at(a, tail, j)] =
-          checked(a, a.table[(size_t)b * a.max_pages + (j - a.freed[b])]);
+      for (int i = base + lane; i < end; i += 32) {
+        const int b = find_owner(cu, b0, b1, i);
+        int32_t* row = a.table + (size_t)b * a.max_pages;
+        if (kind == 1) {
+          const int len = a.seq_lens_out[b] - (a.cu_new[b + 1] - a.cu_new[b]);
+          row[pages_of(len) + (i - cu[b])] = checked(a, a.ring[ring_at(a, head, i)]);
+        } else {
+          a.ring[ring_at(a, tail, i)] = checked(a, row[i - cu[b]]);
+        }
+      }
     }
   }
 }
@@ -290,14 +316,16 @@ cudaError_t launch_tables(const TablesLaunch& a, cudaStream_t s) {
       std::min<long long>((long long)a.batch * a.max_pages, a.ring_capacity);
   const bool alone =
       a.batch <= kAloneBatch && a.slot_capacity <= kAloneTokens && could_free <= kAlonePages;
-  plan_kernel<<<1, kThreads, 0, s>>>(a, alone);
+  const bool small = (long long)a.batch * a.max_pages < 2147483647ll / kPageSize;
+  plan_kernel<<<1, kThreads, 0, s>>>(a, alone, small);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || alone) return e;
-  // a warp per 512 tokens and a thread per page, as far as the host knows them
-  // (the slot map's size, four pages a request), at most eight CTAs per SM
-  const long long guess = a.slot_capacity / (kChunk / 32) + 4ll * a.batch;
-  const int grid = (int)std::max<long long>(
-      1, std::min<long long>((guess + kFillThreads - 1) / kFillThreads, 8ll * sm_count()));
+  // a warp per chunk, as far as the host knows them (the slot map's size, its
+  // pages, four pages a request), at most eight CTAs per SM
+  const long long pages = a.slot_capacity / kPageSize + 4ll * a.batch;
+  const long long chunks = a.slot_capacity / kChunk + pages / kPageChunk + 3;
+  constexpr int kWarps = kFillThreads / 32;
+  const int grid = (int)std::min<long long>((chunks + kWarps - 1) / kWarps, 8ll * sm_count());
   return launch_dependent(fill_kernel, dim3(grid), dim3(kFillThreads), s, a);
 }
 
