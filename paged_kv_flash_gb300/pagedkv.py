@@ -116,7 +116,7 @@ def _check(status: int, what: str):
 
 
 def _need(t: torch.Tensor, dtype, name: str):
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor, got "
                          f"{t.dtype} on {t.device} (contiguous={t.is_contiguous()})")
 
@@ -132,7 +132,7 @@ def _one_device(what: str, *tensors):
     (a pointer of another device would fault there)."""
     now = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != now:
+        if t is not None and t.get_device() != now:
             raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{now}")
 
 
@@ -232,9 +232,10 @@ def kv_append(pool: Pool, k_new, v_new, cu_new, block_table, seq_lens, k_smooth=
     if k_smooth is not None:
         _need(k_smooth, torch.float32, "k_smooth")
     pc = pool.c()
-    st = _lib.pkv_kv_append(ctypes.byref(pc), _ptr(k_new), _ptr(v_new), k_new.shape[0],
-                            _ptr(cu_new), seq_lens.shape[0], _ptr(block_table),
-                            block_table.shape[1], _ptr(seq_lens), _ptr(k_smooth),
+    _one_device("kv_append", pool.k, k_new, v_new, cu_new, block_table, seq_lens, k_smooth)
+    st = _lib.pkv_kv_append(ctypes.byref(pc), k_new.data_ptr(), v_new.data_ptr(), k_new.shape[0],
+                            cu_new.data_ptr(), seq_lens.shape[0], block_table.data_ptr(),
+                            block_table.shape[1], seq_lens.data_ptr(), _ptr(k_smooth),
                             _stream(stream))
     _check(st, "pkv_kv_append")
 
@@ -260,9 +261,9 @@ def kv_unpack(src: Pool, dst: Pool, src_block_table, dst_block_table, seq_lens, 
     sc, dc = src.c(), dst.c()
     _one_device("kv_unpack", src.k, dst.k, src_block_table, dst_block_table, seq_lens, starts,
                 k_smooth)
-    st = _lib.pkv_kv_unpack(ctypes.byref(sc), ctypes.byref(dc), B, _ptr(src_block_table),
-                            src_block_table.shape[1], _ptr(dst_block_table),
-                            dst_block_table.shape[1], _ptr(starts), _ptr(seq_lens),
+    st = _lib.pkv_kv_unpack(ctypes.byref(sc), ctypes.byref(dc), B, src_block_table.data_ptr(),
+                            src_block_table.shape[1], dst_block_table.data_ptr(),
+                            dst_block_table.shape[1], _ptr(starts), seq_lens.data_ptr(),
                             int(max_seq_len), _ptr(k_smooth), _stream(stream))
     _check(st, "pkv_kv_unpack")
 
@@ -287,23 +288,23 @@ def page_tables(seq_lens, new_lens, block_table, free_ring, ring_state, num_page
     for t, n, count in ((seq_lens, "seq_lens", B), (new_lens, "new_lens", B),
                         (ring_state, "ring_state", 2), (seq_lens_out, "seq_lens_out", B),
                         (ring_state_out, "ring_state_out", 2), (cu_new, "cu_new", B + 1),
-                        (page_offsets, "page_offsets", 2 * (B + 1)),
-                        (free_ring, "free_ring", None), (block_table, "block_table", None),
-                        (slot_map, "slot_map", None)):
-        if t is None:
-            continue
-        _need(t, torch.int32, n)
-        if count is not None and t.numel() != count:
+                        (page_offsets, "page_offsets", 2 * (B + 1))):
+        if t.numel() != count:
             raise ValueError(f"{n}: expected {count} entries, got {t.numel()}")
+        _need(t, torch.int32, n)
+    _need(free_ring, torch.int32, "free_ring")
+    _need(block_table, torch.int32, "block_table")
+    if slot_map is not None:
+        _need(slot_map, torch.int32, "slot_map")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table: expected [{B}][max_pages], got {tuple(block_table.shape)}")
     _one_device("page_tables", seq_lens, new_lens, block_table, free_ring, ring_state, cu_new,
                 page_offsets, slot_map, seq_lens_out, ring_state_out)
     st = _lib.pkv_page_tables(
-        _ptr(seq_lens), _ptr(new_lens), B, _ptr(free_ring), free_ring.numel(), _ptr(ring_state),
-        int(num_pages), _ptr(block_table), block_table.shape[1], _ptr(seq_lens_out),
-        _ptr(cu_new), _ptr(page_offsets), _ptr(slot_map),
-        slot_map.numel() if slot_map is not None else 0, _ptr(ring_state_out), _stream(stream))
+        seq_lens.data_ptr(), new_lens.data_ptr(), B, free_ring.data_ptr(), free_ring.numel(),
+        ring_state.data_ptr(), int(num_pages), block_table.data_ptr(), block_table.shape[1], seq_lens_out.data_ptr(),
+        cu_new.data_ptr(), page_offsets.data_ptr(), _ptr(slot_map),
+        slot_map.numel() if slot_map is not None else 0, ring_state_out.data_ptr(), _stream(stream))
     _check(st, "pkv_page_tables")
     return cu_new, seq_lens_out
 
@@ -350,12 +351,14 @@ def paged_attn_decode(pool: Pool, q, block_table, seq_lens, max_seq_len, softmax
     if lse is None and want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     pc = pool.c()
+    _one_device("paged_attn_decode", pool.k, q, block_table, seq_lens, k_smooth, workspace, out,
+                lse)
     fn = _lib.pkv_paged_attn_decode_fused if fused else _lib.pkv_paged_attn_decode
     st = fn(
-        ctypes.byref(pc), _ptr(q), B, Hq, _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), int(max_seq_len), float(softmax_scale), _ptr(k_smooth),
+        ctypes.byref(pc), q.data_ptr(), B, Hq, block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), int(max_seq_len), float(softmax_scale), _ptr(k_smooth),
         int(num_splits), _ptr(workspace), workspace.numel() if workspace is not None else 0,
-        _ptr(out), _ptr(lse), _stream(stream))
+        out.data_ptr(), _ptr(lse), _stream(stream))
     _check(st, "pkv_paged_attn_decode_fused" if fused else "pkv_paged_attn_decode")
     return out, lse
 
@@ -376,10 +379,11 @@ def paged_attn_decode_noalloc(pool: Pool, q, block_table, seq_lens, max_seq_len,
     if lse is None and want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     pc = pool.c()
+    _one_device("paged_attn_decode_noalloc", pool.k, q, block_table, seq_lens, k_smooth, out, lse)
     st = _lib.pkv_paged_attn_decode_noalloc(
-        ctypes.byref(pc), _ptr(q), B, Hq, _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), int(max_seq_len), float(softmax_scale), _ptr(k_smooth),
-        int(num_splits), _ptr(out), _ptr(lse), _stream(stream))
+        ctypes.byref(pc), q.data_ptr(), B, Hq, block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), int(max_seq_len), float(softmax_scale), _ptr(k_smooth),
+        int(num_splits), out.data_ptr(), _ptr(lse), _stream(stream))
     _check(st, "pkv_paged_attn_decode_noalloc")
     return out, lse
 
@@ -420,10 +424,10 @@ def paged_attn_prefill(pool: Pool, q, cu_q, block_table, seq_lens, max_q_len, so
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     pc = pool.c()
     st = _lib.pkv_paged_attn_prefill(
-        ctypes.byref(pc), _ptr(q), T, _ptr(cu_q), seq_lens.shape[0], Hq, _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), int(max_q_len), float(softmax_scale),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), int(num_ctas), _ptr(out),
-        _ptr(lse), _stream(stream))
+        ctypes.byref(pc), q.data_ptr(), T, cu_q.data_ptr(), seq_lens.shape[0], Hq,
+        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), int(max_q_len), float(softmax_scale),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(num_ctas),
+        out.data_ptr(), _ptr(lse), _stream(stream))
     _check(st, "pkv_paged_attn_prefill")
     return out, lse
 
@@ -474,13 +478,16 @@ def paged_attn_decode_multi(pool: Pool, q, cu_q, block_table, seq_lens, max_q_le
         if pool.dtype != INT4:
             raise ValueError("k_smooth: the verify steps of 4-bit pools alone take it")
         _need_smooth(k_smooth)
+    _one_device("paged_attn_decode_multi", pool.k, q, cu_q, block_table, seq_lens, k_smooth,
+                workspace, out, lse)
     int4 = pool.dtype == INT4
     fn = _lib.pkv_paged_attn_decode_multi_int4 if int4 else _lib.pkv_paged_attn_decode_multi
     st = fn(
-        ctypes.byref(pc), _ptr(q), T, _ptr(cu_q), B, Hq, _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), int(max_q_len), int(max_seq_len), float(softmax_scale),
+        ctypes.byref(pc), q.data_ptr(), T, cu_q.data_ptr(), B, Hq, block_table.data_ptr(),
+        block_table.shape[1], seq_lens.data_ptr(), int(max_q_len), int(max_seq_len), float(softmax_scale),
         *((_ptr(k_smooth),) if int4 else ()), int(num_splits),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
+        _ptr(lse),
         _stream(stream))
     _check(st, "pkv_paged_attn_decode_multi_int4" if int4 else "pkv_paged_attn_decode_multi")
     return out, lse
@@ -504,10 +511,10 @@ def qkv_norm_rope_append(pool: Pool, qkv, num_q_heads, cu_new, block_table, seq_
         q_out = torch.empty((T, num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=qkv.device)
     pc = pool.c()
     st = _lib.pkv_qkv_norm_rope_append(
-        ctypes.byref(pc), _ptr(qkv), T, num_q_heads, _ptr(q_norm_w), _ptr(k_norm_w), float(eps),
+        ctypes.byref(pc), qkv.data_ptr(), T, num_q_heads, _ptr(q_norm_w), _ptr(k_norm_w), float(eps),
         _ptr(rope_cos), _ptr(rope_sin), rope_cos.shape[0] if rope_cos is not None else 0,
-        _ptr(cu_new), seq_lens.shape[0], _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-        _ptr(q_out), _stream(stream))
+        cu_new.data_ptr(), seq_lens.shape[0], block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), q_out.data_ptr(), _stream(stream))
     _check(st, "pkv_qkv_norm_rope_append")
     return q_out
 

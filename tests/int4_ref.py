@@ -44,8 +44,8 @@ def values(pool):
     out = np.empty((P, H, 16, 4, 16, 2))
     out[..., 0] = (b & 15).astype(np.float64).transpose(0, 1, 3, 2, 4) - 8
     out[..., 1] = (b >> 4).astype(np.float64).transpose(0, 1, 3, 2, 4) - 8
-    s = np.ascontiguousarray(pool[..., 1024:]).view(np.float16).astype(np.float64)
-    with np.errstate(invalid="ignore"):
+    with np.errstate(invalid="ignore"):                      # NaN scales of unwritten slots
+        s = np.ascontiguousarray(pool[..., 1024:]).view(np.float16).astype(np.float64)
         return (out * s.reshape(P, H, 16, 4, 1, 1)).reshape(P, H, 16, 128)
 
 

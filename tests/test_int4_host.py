@@ -89,6 +89,10 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
     class T:
         def __init__(self, i):
             self.device = torch.device("cuda", i)
+
+        def get_device(self):
+            return self.device.index
+
     pk._one_device("x", T(0), None, T(0))
     with pytest.raises(ValueError, match="cuda:1"):
         pk._one_device("x", T(0), T(1))
