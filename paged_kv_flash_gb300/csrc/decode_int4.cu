@@ -518,21 +518,24 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (!CAREFUL || sees(u, j)) pm[j & 1] = fmaxf(pm[j & 1], s[u][j]);
+    // The maximum moves only when a score passes it by more than 8 (so p <= 2^8):
+    // every lane compares its own, and the reduction over the lanes of a column
+    // waits until one has to move.
+    if (__any_sync(FULL, fmaf(pm[0], sl2[0], -mu[0]) > 8.f || fmaf(pm[1], sl2[1], -mu[1]) > 8.f)) {
 #pragma unroll
-    for (int x = 4; x <= 16; x <<= 1) {
-      pm[0] = fmaxf(pm[0], __shfl_xor_sync(FULL, pm[0], x));
-      pm[1] = fmaxf(pm[1], __shfl_xor_sync(FULL, pm[1], x));
-    }
-    // the maximum moves only when a step passes it by more than 8
-    pm[0] *= sl2[0];
-    pm[1] *= sl2[1];
-    const bool up0 = pm[0] > mu[0] + 8.f, up1 = pm[1] > mu[1] + 8.f;
-    if (__any_sync(FULL, up0 || up1)) {
-      const float f0 = up0 ? fast_exp2(mu[0] - pm[0]) : 1.f;
-      const float f1 = up1 ? fast_exp2(mu[1] - pm[1]) : 1.f;
-      if (up0) mu[0] = pm[0];
-      if (up1) mu[1] = pm[1];
-      rescale(f0, f1);
+      for (int x = 4; x <= 16; x <<= 1) {
+        pm[0] = fmaxf(pm[0], __shfl_xor_sync(FULL, pm[0], x));
+        pm[1] = fmaxf(pm[1], __shfl_xor_sync(FULL, pm[1], x));
+      }
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float top = pm[e] * sl2[e];
+        const bool up = top > mu[e] + 8.f;
+        f[e] = up ? fast_exp2(mu[e] - top) : 1.f;
+        if (up) mu[e] = top;
+      }
+      rescale(f[0], f[1]);
     }
     uint32_t pw[NP][2];
 #pragma unroll
