@@ -21,8 +21,10 @@
 //     gives 0 whatever P' rounds to).
 //
 // One CTA per (split, KV head x row group, sequence), mma.sync m16n8k16, f16
-// in, fp32 out.  A warp takes whole pages of its split, round-robin, from a
-// private ring of shared-memory buffers filled by two bulk copies a page.
+// in, fp32 out.  A warp takes whole pages of its split, round-robin, two at a
+// time, from a private ring of shared-memory buffers that it fills by 16-byte
+// asynchronous copies: nine instructions for two pages, where four bulk copies
+// by one lane (1,152 bytes each) held the warp up for longer.
 // Per page and 8 query rows (n-tile; row = token * G + head):
 //   S^T = K Q^T: A = the page's 16 keys by ldmatrix, one group of 32 channels
 //     per two MMAs, because the group's scale of a key multiplies its partial
@@ -68,8 +70,7 @@ constexpr int kMargin = 3;                          // octaves V scales may grow
 // n-tile's other four columns.
 constexpr int kPlain = 0, kLowApart = 1, kLowBeside = 2;
 
-// Shared memory: barriers (256 bytes), the query's offset fragment and scale
-// factors, then its B fragments (8 k-steps x 32 lanes x 8 bytes, twice with a
+// Shared memory: the query's offset fragment and scale factors, then its B fragments (8 k-steps x 32 lanes x 8 bytes, twice with a
 // low part: in registers they would cost 16 or 32 of them, a CTA per SM,
 // against 4 or 8 loads a page), then the warps' rings.
 constexpr int qfrag_bytes(int low) { return 2048 * (low == kLowApart ? 2 : 1); }
@@ -127,6 +128,11 @@ __device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]),
         "f"(z[3]));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;"
+               ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -246,7 +252,6 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   constexpr uint32_t kEight = 0x48004800u;          // (8, 8) in f16
   pdl_trigger();                                    // the combine may be placed now
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
   uint32_t* s_off = reinterpret_cast<uint32_t*>(smem + 256);            // [lane]
   float* s_back = reinterpret_cast<float*>(smem + 384);                 // [row]
   uint2* qs = reinterpret_cast<uint2*>(smem + 1024);                    // [hi | lo][k-step][lane]
@@ -290,52 +295,48 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   const int L_end = min(L, p_end * kPageSize);      // a step may reach past the split
   const int n_w = max(0, (p_end - p0 + NP * W - 1) / (NP * W));   // steps of this warp
 
-  const uint32_t bar0 = smem_u32(bars + warp * NB);
   uint8_t* wbuf = bufs + (size_t)warp * kWarpBytes;
   const uint32_t wbuf_s = smem_u32(wbuf);
-  if (lane == 0) {
-#pragma unroll
-    for (int k = 0; k < NB; ++k) mbar_init(bar0 + 8 * k, 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
 
   // a cache read by several row groups should stay in L2 for them
   const uint64_t policy = a.row_groups == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
   int ids = 0;
-  const uint8_t* k_head = a.k + (size_t)h * kInt4Slab;
-  const uint8_t* v_head = a.v + (size_t)h * kInt4Slab;
+  // A step's copy: K, V of its first page, K, V of its second, 72 16-byte chunks
+  // each, one behind the other in the buffer, so that chunk 32 i + lane goes to
+  // byte 512 i + 16 lane; instructions 2, 4 and 6 cross from one slab to the next.
+  const uint8_t* k_lane = a.k + (size_t)h * kInt4Slab + lane * 16;
+  const uint8_t* v_lane = a.v + (size_t)h * kInt4Slab + lane * 16;
   const uint32_t page_stride = (uint32_t)a.num_kv_heads * kInt4Slab;
-  auto issue = [&](int j, int t) {                  // step j as the ring's t-th
+  auto issue = [&](int j) {                         // steps go into the ring in order
     constexpr int kSteps = 32 / NP;                 // steps of an id word
-    if (j % kSteps == 0) {
-      const int pg = id_page(j);
-      ids = j == 0 ? bt_first : (pg < p_end ? __ldg(bt_row + pg) : 0);
-      if (pg >= p_end) ids = 0;                     // past the split: any page, never used
-      if (ids < 0 || ids >= a.num_pages) {
-        atomicOr(&g_err_int4, kErrBadIndex);
-        ids = 0;
+    if (j < n_w) {
+      if (j % kSteps == 0) {
+        const int pg = id_page(j);
+        ids = j == 0 ? bt_first : (pg < p_end ? __ldg(bt_row + pg) : 0);
+        if (pg >= p_end) ids = 0;                   // past the split: any page, never used
+        if (ids < 0 || ids >= a.num_pages) {
+          atomicOr(&g_err_int4, kErrBadIndex);
+          ids = 0;
+        }
       }
-    }
-    int id[NP];
+      const uint64_t at0 = (uint64_t)(uint32_t)__shfl_sync(FULL, ids, (j % kSteps) * NP) * page_stride;
+      const uint64_t at1 =
+          (uint64_t)(uint32_t)__shfl_sync(FULL, ids, (j % kSteps) * NP + 1) * page_stride;
+      const uint8_t* k0 = k_lane + at0;
+      const uint8_t* v0 = v_lane + at0 - kInt4Slab;
+      const uint8_t* k1 = k_lane + at1 - 2 * kInt4Slab;
+      const uint8_t* v1 = v_lane + at1 - 3 * kInt4Slab;
+      const uint32_t dst = wbuf_s + (j % NB) * kStepBytes + lane * 16;
+      const uint8_t* from[9] = {k0, k0, lane < 8 ? k0 : v0, v0, lane < 16 ? v0 : k1,
+                                k1, lane < 24 ? k1 : v1, v1, v1};
 #pragma unroll
-    for (int u = 0; u < NP; ++u) id[u] = __shfl_sync(FULL, ids, (j % kSteps) * NP + u);
-    if (lane == 0) {
-      const uint32_t bar = bar0 + 8 * (t % NB), dst = wbuf_s + (t % NB) * kStepBytes;
-      // the warp's reads of this buffer are done (__syncwarp); order them
-      // before the async-proxy refill
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive_expect_tx(bar, kStepBytes);
-#pragma unroll
-      for (int u = 0; u < NP; ++u) {
-        const uint64_t at = (uint64_t)(uint32_t)id[u] * page_stride;
-        bulk_g2s_hint(dst + u * kPageBytes, k_head + at, kInt4Slab, bar, policy);
-        bulk_g2s_hint(dst + u * kPageBytes + kInt4Slab, v_head + at, kInt4Slab, bar, policy);
-      }
+      for (int i = 0; i < 9; ++i) cp_async16(dst + 512 * i, from[i] + 512 * i, policy);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");     // an empty one keeps the count
   };
-  const int pro = min(NB, n_w);
-  for (int j = 0; j < pro; ++j) issue(j, j);
+  static_assert(NP == 2 && kStepBytes == 9 * 512 && kInt4Slab == 72 * 16, "nine copies a lane");
+#pragma unroll 1
+  for (int j = 0; j < NB; ++j) issue(j);
 
   // Query fragments (column r of the n-tile = row row0 + r; kLowBeside: columns
   // 4-7 are the low parts of rows 0-3), made by one warp for all.
@@ -582,47 +583,37 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   // others, whose P' stays finite unless a scale outgrows them and its key's p
   // is near the top.  If O is not finite at the end, a second pass watches
   // every step (a NaN in the cache costs that pass too).
-  int t = 0, t_issued = pro;                        // steps taken from and put into the ring
-  bool failed = false;
-  // step j: waits for its buffer, works on it and refills it with step j + NB
+  // step j: waits for its copy, works on it and refills its buffer with step j + NB
   auto take = [&](int j, auto careful_tag) {
-    if (!__all_sync(FULL, mbar_wait(bar0 + 8 * (t % NB), (uint32_t)(t / NB) & 1u))) {
-      failed = true;
-      return;
-    }
-    const int at = (t % NB) * kStepBytes;
+    asm volatile("cp.async.wait_group %0;" ::"n"(NB - 1) : "memory");
+    __syncwarp();                                   // the other lanes' parts too
+    const int at = (j % NB) * kStepBytes;
     step(wbuf + at, wbuf_s + at, (p0 + NP * W * j) * kPageSize, careful_tag);
     __syncwarp();
-    if (j + NB < n_w) issue(j + NB, t_issued++);
-    ++t;
+    issue(j + NB);
   };
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     reset();
-    if (pass > 0)
-      for (int j = 0; j < pro; ++j) issue(j, t_issued++);
+    if (pass > 0) {
+#pragma unroll 1
+      for (int j = 0; j < NB; ++j) issue(j);
+    }
     int j = 0;
     if (pass == 0 && n_full > 1) {
       take(0, std::true_type{});
       if (vtop + kMargin > vexp) raise_vexp(min(17, vtop + kMargin));
 #pragma unroll 1
-      for (j = 1; j < n_full && !failed; ++j) take(j, std::false_type{});
+      for (j = 1; j < n_full; ++j) take(j, std::false_type{});
     }
 #pragma unroll 1
-    for (; j < n_w && !failed; ++j) take(j, std::true_type{});
-    if (failed) break;
+    for (; j < n_w; ++j) take(j, std::true_type{});
     bool finite = true;
 #pragma unroll
     for (int q = 0; q < 8; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) finite = finite && fabsf(o[q][i]) < INFINITY;
     if (__all_sync(FULL, finite)) break;
-  }
-  if (failed) {
-    if (lane == 0) atomicOr(&g_err_int4, kErrTimeout);
-    // let every copy this warp issued land (bounded) before the buffers are
-    // reused or the CTA exits
-    for (; t < t_issued; ++t) (void)mbar_wait(bar0 + 8 * (t % NB), (uint32_t)(t / NB) & 1u);
   }
   __syncwarp();
 
@@ -642,17 +633,15 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     for (int e = 0; e < 2; ++e) {
       constexpr float k24 = 16777216.f, k20 = 1048576.f;
       const float kk = cs[g >> 1][2 * (g & 1) + e];
-      float4 v = make_float4(o[2 * g][e] * k24 - kk, o[2 * g][2 + e] * k20 - kk,
+      const float4 v = make_float4(o[2 * g][e] * k24 - kk, o[2 * g][2 + e] * k20 - kk,
                              o[2 * g + 1][e] * k24 - kk, o[2 * g + 1][2 + e] * k20 - kk);
-      if (failed) v = make_float4(0.f, 0.f, 0.f, 0.f);
       *reinterpret_cast<float4*>(wo + (2 * qd + e) * kHeadDim + 32 * g + 4 * r) = v;
     }
   if (r == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const bool none = failed || mu[e] == kNoKey;
-      wm[2 * qd + e] = none ? kNoKey : mu[e] + (float)vexp;
-      wl[2 * qd + e] = failed ? 0.f : l[e];
+      wm[2 * qd + e] = mu[e] == kNoKey ? kNoKey : mu[e] + (float)vexp;
+      wl[2 * qd + e] = l[e];
     }
   }
   __syncthreads();
