@@ -65,16 +65,21 @@ static_assert(kRows * (kHeadDim + 2) * 4 <= kWarpBytes, "a warp's results fit it
 constexpr float kNoKey = -1.0e30f;                  // running max before any visible key
 constexpr int kShift = 7;                           // p carries 2^7: P' <= 2^(8 + 7)
 constexpr int kMargin = 3;                          // octaves V scales may grow unwatched
-// How a query with key weights (more bits than f16 holds) is given: not at
-// all; a low part in MMAs of its own; or, with at most four rows, in the
-// n-tile's other four columns.
-constexpr int kPlain = 0, kLowApart = 1, kLowBeside = 2;
+// How the query fills the n-tile's eight columns.  kPlain: eight rows.
+// kLowApart: eight rows with key weights (more bits than f16 holds), the low
+// parts in MMAs of their own.  With at most four rows: kPlainFour, each row
+// twice, and kLowBeside, the high parts and, beside them, the low parts, whose
+// scores are added.  Both halves of the columns then hold the same P, and PV
+// works on two groups at once (see there).
+constexpr int kPlain = 0, kLowApart = 1, kLowBeside = 2, kPlainFour = 3;
+constexpr bool weighted(int mode) { return mode == kLowApart || mode == kLowBeside; }
+constexpr bool four_rows(int mode) { return mode == kLowBeside || mode == kPlainFour; }
 
 // Shared memory: the query's offset fragment and scale factors, then its B fragments (8 k-steps x 32 lanes x 8 bytes, twice with a
 // low part: in registers they would cost 16 or 32 of them, a CTA per SM,
 // against 4 or 8 loads a page), then the warps' rings.
-constexpr int qfrag_bytes(int low) { return 2048 * (low == kLowApart ? 2 : 1); }
-constexpr int smem_of(int low) { return 1024 + qfrag_bytes(low) + W * kWarpBytes; }
+constexpr int qfrag_bytes(int mode) { return 2048 * (mode == kLowApart ? 2 : 1); }
+constexpr int smem_of(int mode) { return 1024 + qfrag_bytes(mode) + W * kWarpBytes; }
 static_assert(kCtasPerSm * (smem_of(kLowApart) + 1024) <= 228 * 1024, "resident CTAs");
 
 // Where all CTAs of a call are resident at once, up to this many splits of a
@@ -181,10 +186,10 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
 // fragment of -8 sum(q) of the four groups, f16 high parts in rows 0-3 and low
 // parts in rows 4-7 (good to 2^-22).  Returns the power of two that undoes the
 // scaling.
-template <int LOW>
+template <int MODE>
 __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const float* w, float sign,
                                              int qd, uint32_t (&hi)[8][2],
-                                             uint32_t (&lo)[LOW ? 8 : 1][2], uint32_t& off) {
+                                             uint32_t (&lo)[weighted(MODE) ? 8 : 1][2], uint32_t& off) {
   float x[4][8];
   float top = 0.f;
 #pragma unroll
@@ -197,7 +202,7 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
       x[g][2 * e] = bf16lo(r4[e]);
       x[g][2 * e + 1] = bf16hi(r4[e]);
     }
-    if constexpr (LOW != kPlain) {
+    if constexpr (weighted(MODE)) {
       const float4* ws = reinterpret_cast<const float4*>(w + 32 * g + 8 * qd);
       const float4 w0 = __ldg(ws), w1 = __ldg(ws + 1);
       x[g][0] *= w0.x, x[g][1] *= w0.y, x[g][2] *= w0.z, x[g][3] *= w0.w;
@@ -225,7 +230,7 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
         const float2 h = halves(h2);
         float both = h.x + h.y;
         hi[2 * g + s][j] = h2;
-        if constexpr (LOW != kPlain) {
+        if constexpr (weighted(MODE)) {
           const uint32_t l2 = pack_f16x2(y0 - h.x, y1 - h.y);
           const float2 l = halves(l2);
           lo[2 * g + s][j] = l2;
@@ -244,7 +249,7 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
   return __int_as_float((127 - sh) << 23);
 }
 
-template <int LOW>
+template <int MODE>
 __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     decode_int4_kernel(const __grid_constant__ Launch a) {
   constexpr uint32_t FULL = 0xffffffffu;
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   uint32_t* s_off = reinterpret_cast<uint32_t*>(smem + 256);            // [lane]
   float* s_back = reinterpret_cast<float*>(smem + 384);                 // [row]
   uint2* qs = reinterpret_cast<uint2*>(smem + 1024);                    // [hi | lo][k-step][lane]
-  uint8_t* bufs = smem + 1024 + qfrag_bytes(LOW);
+  uint8_t* bufs = smem + 1024 + qfrag_bytes(MODE);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, qd = lane & 3;
@@ -338,23 +343,23 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
 #pragma unroll 1
   for (int j = 0; j < NB; ++j) issue(j);
 
-  // Query fragments (column r of the n-tile = row row0 + r; kLowBeside: columns
-  // 4-7 are the low parts of rows 0-3), made by one warp for all.
+  // Query fragments (column r of the n-tile = row row0 + r; four rows: columns
+  // 4-7 are rows 0-3 again, or their low parts), made by one warp for all.
   if (warp == W - 1) {
-    uint32_t hi[8][2], lo[LOW ? 8 : 1][2], off;
-    const int rq = row0 + (LOW == kLowBeside ? r & 3 : r);
+    uint32_t hi[8][2], lo[weighted(MODE) ? 8 : 1][2], off;
+    const int rq = row0 + (four_rows(MODE) ? r & 3 : r);
     const __nv_bfloat16* q =
         rq < R ? a.q + ((size_t)(q0 + rq / G) * Hq + h * G + rq % G) * kHeadDim : nullptr;
     const float back =
-        query_frags<LOW>(q, a.k_smooth, a.softmax_scale < 0.f ? -1.f : 1.f, qd, hi, lo, off);
-    const bool low = LOW == kLowBeside && r >= 4;
+        query_frags<MODE>(q, a.k_smooth, a.softmax_scale < 0.f ? -1.f : 1.f, qd, hi, lo, off);
+    const bool low = MODE == kLowBeside && r >= 4;
     s_off[lane] = low ? 0u : off;
     if (qd == 0) s_back[r] = back;
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       qs[ks * 32 + lane] =
-          low ? make_uint2(lo[LOW ? ks : 0][0], lo[LOW ? ks : 0][1]) : make_uint2(hi[ks][0], hi[ks][1]);
-      if constexpr (LOW == kLowApart) qs[(8 + ks) * 32 + lane] = make_uint2(lo[ks][0], lo[ks][1]);
+          low ? make_uint2(lo[weighted(MODE) ? ks : 0][0], lo[weighted(MODE) ? ks : 0][1]) : make_uint2(hi[ks][0], hi[ks][1]);
+      if constexpr (MODE == kLowApart) qs[(8 + ks) * 32 + lane] = make_uint2(lo[ks][0], lo[ks][1]);
     }
   }
   __syncthreads();
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   int lim[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int c = 2 * qd + e, rho = row0 + (LOW == kLowBeside ? c & 3 : c);
+    const int c = 2 * qd + e, rho = row0 + (four_rows(MODE) ? c & 3 : c);
     sl2[e] = fabsf(a.softmax_scale) * (kLog2e * 16777216.f) * s_back[c];
     lim[e] = min(L_end - 1, rho < R ? L - qn + rho / G : L - 1);
   }
@@ -375,11 +380,15 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   const int spare = lim_min + 1 - p0 * kPageSize;   // keys that all see, from step 0 on
   const int n_full = min(n_w, max(0, (spare + (W - 1) * kStepKeys) / (W * kStepKeys)));
 
-  // O^T of group g, half t: channels 32 g + 4 r + 2 t (o[..][0..1]) and + 1
-  // (o[..][2..3], times 16) of columns 2 qd, 2 qd + 1, in units of 2^-24 and with
-  // the codes' offset of 8; cs[g2]: 8 sum(P') of groups 2 g2 ([0..1]) and 2 g2 + 1
-  // ([2..3]).  mu: the maximum the exponentials are taken against; p carries
-  // 2^(kShift - vexp); sub = kShift - vexp - mu.
+  // O^T, in units of 2^-24 and with the codes' offset of 8, columns 2 qd and
+  // 2 qd + 1.  Eight rows: o[2 g + t] = channels 32 g + 4 r + 2 t ([0..1]) and + 1
+  // ([2..3], times 16) of group g.  Four rows: o[4 g2 + i] = channel 4 r + i (times
+  // 16 for odd i) of group 2 g2 ([0..1], columns 0-3) and 2 g2 + 1 ([2..3],
+  // columns 4-7; the other halves are products of one group's codes with the
+  // other's P' and go nowhere).  cs[g2]: 8 sum(P') of groups 2 g2 ([0..1]) and
+  // 2 g2 + 1 ([2..3]); four rows: of the column's own group, twice.  mu: the
+  // maximum the exponentials are taken against; p carries 2^(kShift - vexp); sub
+  // = kShift - vexp - mu.
   float o[8][4], cs[2][4], mu[2], sub[2], l[2];
   int vexp, vtop;
   auto reset = [&]() {
@@ -423,6 +432,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   float zero[4];                                    // opaque, so that they stay in registers
 #pragma unroll
   for (int j = 0; j < 4; ++j) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[j]));
+  const uint32_t my_sel = r < 4 ? 0x5410u : 0x7632u;  // four rows: this column's group of a pair
   // slot order of the MMA rows: row i = slot 2 i, row 8 + i = slot 2 i + 1, so
   // that a lane's scales are 16 contiguous bytes
   const int ld_row = (lane >> 4) * 256 + (2 * (lane & 7) + ((lane >> 3) & 1)) * 16;
@@ -454,7 +464,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
         const int g = 2 * g2 + w;
         const uint2 qa = qs[(2 * g) * 32 + lane], qb = qs[(2 * g + 1) * 32 + lane];
         uint2 la = make_uint2(0u, 0u), lb = la;
-        if constexpr (LOW == kLowApart) {
+        if constexpr (MODE == kLowApart) {
           la = qs[(8 + 2 * g) * 32 + lane];
           lb = qs[(9 + 2 * g) * 32 + lane];
         }
@@ -467,7 +477,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
           float d[4];
           mma_f16_new(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, qa.x, qa.y, zero);
           mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, qb.x, qb.y);
-          if constexpr (LOW == kLowApart) {
+          if constexpr (MODE == kLowApart) {
             mma_f16(d, w0 & NIB0, w1 & NIB0, w0 & NIB1, w1 & NIB1, la.x, la.y);
             mma_f16(d, x0 & NIB0, x1 & NIB0, x0 & NIB1, x1 & NIB1, lb.x, lb.y);
           }
@@ -478,7 +488,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
         }
       }
     }
-    if constexpr (LOW == kLowBeside) {                 // high + low columns, in both
+    if constexpr (MODE == kLowBeside) {                 // high + low columns, in both
 #pragma unroll
       for (int u = 0; u < NP; ++u)
 #pragma unroll
@@ -553,27 +563,45 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
       pw[u][1] = movm_t(pack_f16x2(p[2], p[3]));
     }
 
-    // O += V P', cs += 8 P', group by group
+    // O += V P', cs += 8 P'.  Eight rows: group by group, an A tile of two
+    // channels of each of eight quads.  Four rows: two groups at a time, an A tile
+    // of one channel of each quad of both, the first group's P' in columns 0-3,
+    // the second's in 4-7: as many MMAs for O, half as many for cs, half the
+    // scaling of P.
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const uint32_t vcs = kst + u * kPageBytes + kInt4Slab;
 #pragma unroll
       for (int g2 = 0; g2 < 2; ++g2) {
-        uint32_t vw[4];
+        uint32_t vw[4];              // slots 4 qd, 4 qd + 2 and + 1, + 3 of group 2 g2, then 2 g2 + 1
         ldsm_x4_t(vcs + g2 * 512 + ld_row, vw);
+        const uint32_t sa0 = g2 ? va[u].y : va[u].x, sa1 = g2 ? vb[u].y : vb[u].x;
+        const uint32_t sb0 = g2 ? va[u].w : va[u].z, sb1 = g2 ? vb[u].w : vb[u].z;
+        if constexpr (four_rows(MODE)) {
+          const uint32_t pb0 = mul_f16x2(pw[u][0], __byte_perm(sa0, sa1, my_sel));
+          const uint32_t pb1 = mul_f16x2(pw[u][1], __byte_perm(sb0, sb1, my_sel));
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int g = 2 * g2 + w;
-          const uint32_t w0 = vw[2 * w], w1 = vw[2 * w + 1];
-          const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
-          const uint32_t sel = w ? 0x7632u : 0x5410u;    // group g of two slots' words
-          const uint32_t sa = __byte_perm(g2 ? va[u].y : va[u].x, g2 ? vb[u].y : vb[u].x, sel);
-          const uint32_t sb = __byte_perm(g2 ? va[u].w : va[u].z, g2 ? vb[u].w : vb[u].z, sel);
-          const uint32_t pb0 = mul_f16x2(pw[u][0], sa), pb1 = mul_f16x2(pw[u][1], sb);
-          mma_f16(o[2 * g], w0 & NIB0, w0 & NIB1, w1 & NIB0, w1 & NIB1, pb0, pb1);
-          mma_f16(o[2 * g + 1], x0 & NIB0, x0 & NIB1, x1 & NIB0, x1 & NIB1, pb0, pb1);
-          mma_f16(cs[g2], w ? 0u : kEight, w ? kEight : 0u, w ? 0u : kEight, w ? kEight : 0u, pb0,
-                  pb1);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w0 = i ? vw[0] >> 8 : vw[0], w1 = i ? vw[1] >> 8 : vw[1];
+            const uint32_t x0 = i ? vw[2] >> 8 : vw[2], x1 = i ? vw[3] >> 8 : vw[3];
+            mma_f16(o[4 * g2 + 2 * i], w0 & NIB0, x0 & NIB0, w1 & NIB0, x1 & NIB0, pb0, pb1);
+            mma_f16(o[4 * g2 + 2 * i + 1], w0 & NIB1, x0 & NIB1, w1 & NIB1, x1 & NIB1, pb0, pb1);
+          }
+          mma_f16(cs[g2], kEight, kEight, kEight, kEight, pb0, pb1);
+        } else {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int g = 2 * g2 + w;
+            const uint32_t w0 = vw[2 * w], w1 = vw[2 * w + 1];
+            const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
+            const uint32_t sel = w ? 0x7632u : 0x5410u;    // group g of two slots' words
+            const uint32_t pb0 = mul_f16x2(pw[u][0], __byte_perm(sa0, sa1, sel));
+            const uint32_t pb1 = mul_f16x2(pw[u][1], __byte_perm(sb0, sb1, sel));
+            mma_f16(o[2 * g], w0 & NIB0, w0 & NIB1, w1 & NIB0, w1 & NIB1, pb0, pb1);
+            mma_f16(o[2 * g + 1], x0 & NIB0, x0 & NIB1, x1 & NIB0, x1 & NIB1, pb0, pb1);
+            mma_f16(cs[g2], w ? 0u : kEight, w ? kEight : 0u, w ? 0u : kEight, w ? kEight : 0u,
+                    pb0, pb1);
+          }
         }
       }
     }
@@ -627,16 +655,32 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     l[0] += __shfl_xor_sync(FULL, l[0], x);
     l[1] += __shfl_xor_sync(FULL, l[1], x);
   }
+  constexpr float k24 = 16777216.f, k20 = 1048576.f;
+  if constexpr (four_rows(MODE)) {
+    const bool second = qd >= 2;                    // columns 4-7: the pairs' second groups
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
+    for (int g2 = 0; g2 < 2; ++g2)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      constexpr float k24 = 16777216.f, k20 = 1048576.f;
-      const float kk = cs[g >> 1][2 * (g & 1) + e];
-      const float4 v = make_float4(o[2 * g][e] * k24 - kk, o[2 * g][2 + e] * k20 - kk,
-                             o[2 * g + 1][e] * k24 - kk, o[2 * g + 1][2 + e] * k20 - kk);
-      *reinterpret_cast<float4*>(wo + (2 * qd + e) * kHeadDim + 32 * g + 4 * r) = v;
-    }
+      for (int e = 0; e < 2; ++e) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = (second ? o[4 * g2 + i][2 + e] : o[4 * g2 + i][e]) * ((i & 1) ? k20 : k24) -
+                 cs[g2][e];
+        *reinterpret_cast<float4*>(wo + (2 * (qd & 1) + e) * kHeadDim + 32 * (2 * g2 + second) +
+                                   4 * r) = make_float4(x[0], x[1], x[2], x[3]);
+      }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float kk = cs[g >> 1][2 * (g & 1) + e];
+        *reinterpret_cast<float4*>(wo + (2 * qd + e) * kHeadDim + 32 * g + 4 * r) =
+            make_float4(o[2 * g][e] * k24 - kk, o[2 * g][2 + e] * k20 - kk,
+                        o[2 * g + 1][e] * k24 - kk, o[2 * g + 1][2 + e] * k20 - kk);
+      }
+  }
   if (r == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -744,11 +788,11 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   }
 }
 
-template <int LOW>
+template <int MODE>
 cudaError_t launch_as(const Launch& a, int batch, cudaStream_t s) {
-  constexpr int smem = smem_of(LOW);
+  constexpr int smem = smem_of(MODE);
   cudaError_t e = pkv_host::set_max_dynamic_smem(
-      reinterpret_cast<const void*>(decode_int4_kernel<LOW>), smem);
+      reinterpret_cast<const void*>(decode_int4_kernel<MODE>), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.splits, a.num_kv_heads * a.row_groups, batch);
@@ -763,15 +807,16 @@ cudaError_t launch_as(const Launch& a, int batch, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, decode_int4_kernel<LOW>, a);
+  return cudaLaunchKernelEx(&cfg, decode_int4_kernel<MODE>, a);
 }
 
 cudaError_t launch_rows(Launch& a, int rows, int batch, cudaStream_t s) {
   a.row_groups = (rows + kRows - 1) / kRows;
   a.clustered = pkv_host::int4_merges_itself(
       a.splits, pkv_host::int4_units(batch, a.num_kv_heads, rows));
-  if (!a.k_smooth) return launch_as<kPlain>(a, batch, s);
-  return rows <= kRows / 2 ? launch_as<kLowBeside>(a, batch, s) : launch_as<kLowApart>(a, batch, s);
+  if (rows <= kRows / 2)
+    return a.k_smooth ? launch_as<kLowBeside>(a, batch, s) : launch_as<kPlainFour>(a, batch, s);
+  return a.k_smooth ? launch_as<kLowApart>(a, batch, s) : launch_as<kPlain>(a, batch, s);
 }
 
 }  // namespace
