@@ -109,17 +109,28 @@ struct Plan {
 
 // Quantised pools: longer splits, a full wave of CTAs.  INT4 (four CTAs
 // resident per SM, eight pages a round of a CTA's warps): work that would give
-// splits of the most pages takes longer ones still where those make a single
-// wave (eight 32k-position sequences: 9 splits of 232 pages 66.8 us, 16 of 128
-// 68.6 us, 12 of 176, a wave and a quarter, 76.8 us).
-constexpr int kInt4Round = 8, kInt4WaveMaxPages = 256;
+// splits of the most pages takes such splits as make one wave that fills 85 % of
+// the places, where there are any (eight 32k-position sequences: 9 splits of 232
+// pages 57 us, 16 of 128 59 us, 12 of 176, a wave and a quarter, 65 us).  Sharing
+// all pages of a ragged batch out evenly over one wave of CTAs, unit by unit, was
+// no faster than the grid of 128-page splits (64 sequences of 512..8,192
+// positions: 72.6 us against 73.8 us).
+constexpr int kInt4Round = 8;
 
 // Pages per split with which `units` work items of mp pages make one wave of
 // int4 CTAs.
 int int4_wave_pages(long long units, int mp) {
-  const long long s1 = std::max<long long>(1, (long long)sm_count() * pkv_host::kInt4CtasPerSm / units);
+  const long long places = (long long)sm_count() * pkv_host::kInt4CtasPerSm;
+  const long long s1 = std::max<long long>(1, places / std::max<long long>(1, units));
   const long long c = (mp + s1 - 1) / s1;
   return (int)((c + kInt4Round - 1) / kInt4Round * kInt4Round);
+}
+
+// Whether splits of that size are one wave that fills 85 % of the places.
+bool int4_wave_fits(long long units, int mp, int pages) {
+  const long long ctas = units * ((mp + pages - 1) / pages);
+  const long long places = (long long)sm_count() * pkv_host::kInt4CtasPerSm;
+  return ctas <= places && ctas * 100 >= places * 85;
 }
 
 Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, int num_splits,
@@ -140,9 +151,10 @@ Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, in
     const int round = dtype == PKV_INT4 ? kInt4Round : pkv_host::kDecodeWarps;
     c = (c + round - 1) / round * round;
     if (dtype == PKV_INT4 && c >= kPlanMaxPages) {
-      const int wave = int4_wave_pages(
-          pkv_host::int4_units(batch, num_kv_heads, num_q_heads / num_kv_heads), mp);
-      if (wave <= kInt4WaveMaxPages) c = std::max<long long>(c, wave);
+      const long long units =
+          pkv_host::int4_units(batch, num_kv_heads, num_q_heads / num_kv_heads);
+      const int wave = int4_wave_pages(units, mp);
+      if (int4_wave_fits(units, mp, wave)) c = wave;
     }
     C = (int)std::min<long long>(c, mp);
   }
@@ -165,10 +177,10 @@ Plan make_plan(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, in
 }
 
 // What the int4 kernel asks of a call: 16-byte loads of queries and weights,
-// and one CTA per 8 query rows of a KV head in the grid's y.
+// and at most 65,535 units (KV head, 8 rows) per sequence.
 pkv_status check_int4(const void* q, const float* k_smooth, int num_kv_heads, int rows) {
   if (!aligned(q, 16) || (k_smooth && !aligned(k_smooth, 16))) return PKV_ERR_INVALID;
-  if ((long long)num_kv_heads * (((long long)rows + 7) / 8) > 65535) return PKV_ERR_UNSUPPORTED;
+  if (pkv_host::int4_units(1, num_kv_heads, rows) > 65535) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
 
@@ -376,7 +388,9 @@ static pkv_status decode_call(const pkv_pool* pool, const void* q, int32_t batch
                            pool->dtype);
   if (p.ws_bytes > 0 && (!workspace || workspace_bytes < p.ws_bytes || !aligned(workspace, 256)))
     return PKV_ERR_INVALID;
-  if ((long long)batch > 65535 || p.splits > 2147483647 / 2) return PKV_ERR_UNSUPPORTED;
+  if ((long long)batch > 65535 || p.splits > 2147483647 / 2 ||
+      (pool->dtype == PKV_INT4 && p.splits > 65535))
+    return PKV_ERR_UNSUPPORTED;
   pkv_host::DecodeLaunch a{};
   a.k = pool->k;
   a.v = pool->v;
@@ -648,7 +662,8 @@ static pkv_status multi_call(const pkv_pool* pool, int32_t dtype, const void* q,
       (!workspace || workspace_bytes < m.p.ws_bytes || !aligned(workspace, 256)))
     return PKV_ERR_INVALID;
   if ((long long)batch > 65535 || (long long)pool->num_kv_heads * m.row_groups > 65535 ||
-      (long long)total_q * num_q_heads > 2147483647ll / 2 || m.p.splits > 2147483647 / 2)
+      (long long)total_q * num_q_heads > 2147483647ll / 2 || m.p.splits > 2147483647 / 2 ||
+      (int4 && m.p.splits > 65535))
     return PKV_ERR_UNSUPPORTED;
   pkv_host::MultiLaunch a{};
   a.k = pool->k;

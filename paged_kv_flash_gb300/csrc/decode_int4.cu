@@ -264,8 +264,10 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, qd = lane & 3;
-  const int split = blockIdx.x, b = blockIdx.z;
-  const int h = blockIdx.y / a.row_groups, rg = blockIdx.y % a.row_groups;
+  // a wave of CTAs is one split of all heads and sequences: the few splits that only
+  // the longest sequences have come last
+  const int split = blockIdx.z, b = blockIdx.y;
+  const int h = blockIdx.x / a.row_groups, rg = blockIdx.x % a.row_groups;
   const int Hq = a.num_q_heads, G = a.group;
 
   // The length, this warp's first 32 page ids and the rows' offsets go out
@@ -795,15 +797,15 @@ cudaError_t launch_as(const Launch& a, int batch, cudaStream_t s) {
       reinterpret_cast<const void*>(decode_int4_kernel<MODE>), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.splits, a.num_kv_heads * a.row_groups, batch);
+  cfg.gridDim = dim3(a.num_kv_heads * a.row_groups, batch, a.splits);
   cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   if (a.clustered) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = a.splits;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }

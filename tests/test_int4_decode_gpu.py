@@ -365,3 +365,102 @@ def test_append_decode_verify_run_together(pk):
             close(out, ro, mag, what=str(new))
             check_lse(lse, rl, str(new))
         assert pk.poll_device_error() == pk.OK
+
+
+# ------------------------------------------------- more than one wave of CTAs
+
+def long_batch(seed, B, lens_of, Hq, Hkv, counts=None, smooth=False):
+    """More work than one wave of CTAs: B sequences whose cached positions share
+    a few pages of random data (the block tables repeat them), so that the
+    float64 reference stays small."""
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens_of(rng, B), np.int32)
+    c = Case(seed, [16 * 24], Hq, Hkv, counts=[1], smooth=smooth)
+    table = rng.choice(c.layout.block_table[0], (B, -(-int(lens.max()) // 16))).astype(np.int32)
+    c.layout = W.Layout(c.layout.num_pages, table, c.layout.sentinel_page)
+    c.lens = lens
+    c.counts = np.ones(B, np.int64) if counts is None else np.asarray(counts)
+    c.cu = W.cu_from_counts(c.counts)
+    c.q = W.normal_bf16(rng, (int(c.counts.sum()), Hq, 128))
+    return c
+
+
+def sampled_ref(c, rows):
+    """The reference of some rows (token t of sequence b alone)."""
+    out, lse, mag = [], [], []
+    for t in rows:
+        b = int(np.searchsorted(c.cu, t, side="right")) - 1
+        n = int(c.lens[b] - c.counts[b] + (t - c.cu[b]) + 1)
+        o = R.attention(c.k, c.v, W.bits_to_float(c.q[t:t + 1]).astype(np.float64), [0, 1],
+                        c.layout.block_table[b:b + 1], [n], SCALE, c.w)
+        for acc, x in zip((out, lse, mag), o):
+            acc.append(x[0])
+    return np.stack(out), np.stack(lse), np.stack(mag)
+
+
+LENGTHS = {
+    "ragged": lambda rng, B: rng.integers(0, 4200, B),
+    "one long": lambda rng, B: np.where(np.arange(B) == B // 2, 20000, rng.integers(0, 40, B)),
+    "zeros between": lambda rng, B: np.where(np.arange(B) % 3 == 1, 3000, 0),
+    "equal": lambda rng, B: np.full(B, 3333),
+}
+
+
+@pytest.mark.parametrize("G,smooth", [(4, False), (4, True), (8, False), (12, True)])
+@pytest.mark.parametrize("kind", sorted(LENGTHS))
+def test_large_batches(pk, kind, G, smooth):
+    B, Hkv = 90, 8
+    c = long_batch(2600 + G, B, LENGTHS[kind], G * Hkv, Hkv, smooth=smooth)
+    out, lse = c.decode(pk)
+    rows = np.unique(np.concatenate([np.random.default_rng(7).integers(0, B, 10),
+                                     np.flatnonzero(c.lens == 0)[:2], [c.lens.argmax(), B - 1]]))
+    ro, rl, mag = sampled_ref(c, rows)
+    idx = torch.from_numpy(rows).cuda()
+    close(out[idx], ro, mag, what=kind)
+    check_lse(lse[idx], rl, kind)
+    # every row, the sampled ones or not, as other splits give it
+    fo, fl = c.decode(pk, fused=True)
+    assert torch.equal(out, fo) and torch.equal(lse, fl)
+    # (the call without workspace takes fewer splits where its 16 MiB are short)
+    for go, gl in (c.decode(pk, 3), c.decode(pk, fn="paged_attn_decode_noalloc")):
+        d = (out.float() - go.float()).abs()
+        assert (d <= 2.0 ** -7 * go.float().abs() + 2 * 2.7e-3 * 6).all()
+        same = torch.isneginf(lse) & torch.isneginf(gl)
+        assert ((lse - gl).abs().masked_fill(same, 0) <= 2e-3).all()
+
+
+@pytest.mark.parametrize("smooth", [False, True])
+def test_large_batches_of_verify_steps(pk, smooth):
+    """Ragged steps (none, one, many tokens; one to eight row groups) and lengths."""
+    rng = np.random.default_rng(2700)
+    B, Hkv, G = 30, 8, 4
+    counts = rng.integers(0, 17, B)
+    counts[:3] = [0, 16, 1]
+    c = long_batch(2701, B, lambda r, n: np.maximum(r.integers(1, 4000, n), counts), G * Hkv, Hkv,
+                   counts=counts, smooth=smooth)
+    out, lse = c.multi(pk, max_q=16)
+    rows = np.unique(np.concatenate([c.cu[:-1][counts > 0][:8], c.cu[1:][counts > 0][:8] - 1]))
+    ro, rl, mag = sampled_ref(c, rows)
+    idx = torch.from_numpy(rows.astype(np.int64)).cuda()
+    close(out[idx], ro, mag)
+    check_lse(lse[idx], rl)
+    go, gl = c.multi(pk, 3, max_q=16)
+    assert ((out.float() - go.float()).abs() <= 2.0 ** -7 * go.float().abs() + 2 * 2.7e-3 * 6).all()
+    assert ((lse - gl).abs() <= 2e-3).all()
+
+
+def test_bad_sequences_in_a_large_batch_leave_the_rest_right(pk):
+    c = long_batch(2800, 90, LENGTHS["ragged"], 32, 8)
+    c.lens[:] = np.maximum(c.lens, 1)
+    good, _ = c.decode(pk)
+    pool, q, bt, lens, ml = c.args(pk)
+    lens[5], bt[7, 0] = -1, pool.num_pages
+    lens[6] = bt.shape[1] * 16 + 1
+    out, lse = pk.paged_attn_decode(pool, q, bt, lens, ml, SCALE)
+    assert pk.poll_device_error() == pk.ERR_INVALID
+    assert pk.poll_device_error() == pk.OK
+    keep = torch.ones(90, dtype=torch.bool, device="cuda")
+    keep[5:8] = False
+    d = (out.float() - good.float()).abs()[keep]
+    assert (d <= 2.0 ** -7 * good.float().abs()[keep] + 2 * 2.7e-3 * 6).all()
+    assert (out[5:7] == 0).all() and torch.isneginf(lse[5:7]).all()
