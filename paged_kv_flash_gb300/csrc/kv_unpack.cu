@@ -6,7 +6,7 @@
 // Bound by memory: a (page, KV head) reads 2 x 1,152 bytes (INT4) or 2 x 2,112
 // (INT8) and writes 2 x 4,096.  One warp per (sequence, page, KV head): 16
 // lanes hold a row's 128 channels, 8 each, so every store instruction writes
-// two whole 256-byte rows, and all loads of a slab go out before its stores.
+// two whole 256-byte rows, and all loads of K and V go out before the stores.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -28,52 +28,63 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
-// K or V of one (page, head): this lane's 8 channels of rows 2j + (lane >> 4),
-// j = 0 .. 7, for rows lo <= row < hi.
-template <bool INT4, bool SMOOTH>
-__device__ __forceinline__ void unpack_slab(const void* src, const float* scales, size_t slab,
-                                            uint4* __restrict__ dst, int lo, int hi,
-                                            const float (&w)[8], int lane) {
-  const int i = lane & 15, half = lane >> 4;
+// K or V of one (page, head) in registers: of rows 2j + (lane >> 4), j = 0 .. 7,
+// this lane's 8 channels' codes; of all rows, a word of the scales (INT4: rows
+// lane / 2, two groups; INT8: row lane % 16).
+template <bool INT4>
+struct Slab {
   uint2 code[8];
-  float sc[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int row = 2 * j + half;
-    code[j] = make_uint2(0u, 0u);
-    sc[j] = 0.f;
-    if (row < lo || row >= hi) continue;
+  uint32_t scale;
+
+  __device__ __forceinline__ void load(const void* src, const float* scales, size_t slab, int lane) {
+    const int i = lane & 15, half = lane >> 4;
     if constexpr (INT4) {
       const uint8_t* base = static_cast<const uint8_t*>(src) + slab * kInt4Slab;
-      const int g = i >> 2;
-      code[j].x = __ldg(reinterpret_cast<const uint32_t*>(base + g * 256 + row * 16 + (i & 3) * 4));
-      sc[j] = __half2float(__ushort_as_half(__ldg(
-          reinterpret_cast<const unsigned short*>(base + kInt4Codes + row * 8 + g * 2))));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        code[j].x = __ldg(reinterpret_cast<const uint32_t*>(base + (i >> 2) * 256 +
+                                                            (2 * j + half) * 16 + (i & 3) * 4));
+      scale = __ldg(reinterpret_cast<const uint32_t*>(base + kInt4Codes) + lane);
     } else {
       const uint8_t* base = static_cast<const uint8_t*>(src) + slab * (kPageSize * kHeadDim);
-      code[j] = __ldg(reinterpret_cast<const uint2*>(base + row * kHeadDim + i * 8));
-      sc[j] = __ldg(scales + slab * kPageSize + row);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        code[j] = __ldg(reinterpret_cast<const uint2*>(base + (2 * j + half) * kHeadDim + i * 8));
+      scale = __float_as_uint(__ldg(scales + slab * kPageSize + i));
     }
   }
+
+  // Rows lo <= row < hi to dst.
+  template <bool SMOOTH>
+  __device__ __forceinline__ void store(uint4* __restrict__ dst, int lo, int hi,
+                                        const float (&w)[8], int lane) const {
+    const int i = lane & 15, half = lane >> 4;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int row = 2 * j + half;
-    if (row < lo || row >= hi) continue;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      int c;
+    for (int j = 0; j < 8; ++j) {
+      const int row = 2 * j + half, g = i >> 2;
+      const uint32_t word = __shfl_sync(0xffffffffu, scale, INT4 ? 2 * row + (g >> 1) : row);
+      if (row < lo || row >= hi) continue;
+      float sc;
       if constexpr (INT4)
-        c = (int)((code[j].x >> (4 * e)) & 15u) - 8;
+        sc = __half2float(__ushort_as_half((unsigned short)((g & 1) ? word >> 16 : word & 0xffffu)));
       else
-        c = (int)(int8_t)(((e < 4 ? code[j].x : code[j].y) >> (8 * (e & 3))) & 0xffu);
-      x[e] = __fmul_rn((float)c, sc[j]);
-      if constexpr (SMOOTH) x[e] = __fmul_rn(x[e], w[e]);
+        sc = __uint_as_float(word);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        int c;
+        if constexpr (INT4)
+          c = (int)((code[j].x >> (4 * e)) & 15u) - 8;
+        else
+          c = (int)(int8_t)(((e < 4 ? code[j].x : code[j].y) >> (8 * (e & 3))) & 0xffu);
+        x[e] = __fmul_rn((float)c, sc);
+        if constexpr (SMOOTH) x[e] = __fmul_rn(x[e], w[e]);
+      }
+      dst[row * 16 + i] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
+                                     pack2(x[6], x[7]));
     }
-    dst[row * 16 + i] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
-                                   pack2(x[6], x[7]));
   }
-}
+};
 
 template <bool INT4>
 __global__ void __launch_bounds__(kWarps * 32)
@@ -107,14 +118,16 @@ __global__ void __launch_bounds__(kWarps * 32)
       continue;
     }
     const size_t slab = (size_t)ps * a.num_kv_heads + h;
-    const size_t out = ((size_t)pd * a.num_kv_heads + h) * (kPageSize * kHeadDim / 8);   // 16-byte units
-    uint4* k_out = static_cast<uint4*>(a.k_out) + out;
+    const size_t out = ((size_t)pd * a.num_kv_heads + h) * (kPageSize * kHeadDim / 8);   // uint4s
+    // slots outside lo .. hi - 1 are loaded too: all of a slab is the pool's
+    Slab<INT4> ks, vs;
+    ks.load(a.k, a.k_scale, slab, lane);
+    vs.load(a.v, a.v_scale, slab, lane);
     if (a.k_smooth)
-      unpack_slab<INT4, true>(a.k, a.k_scale, slab, k_out, lo, hi, w, lane);
+      ks.template store<true>(static_cast<uint4*>(a.k_out) + out, lo, hi, w, lane);
     else
-      unpack_slab<INT4, false>(a.k, a.k_scale, slab, k_out, lo, hi, w, lane);
-    unpack_slab<INT4, false>(a.v, a.v_scale, slab, static_cast<uint4*>(a.v_out) + out, lo, hi, w,
-                             lane);
+      ks.template store<false>(static_cast<uint4*>(a.k_out) + out, lo, hi, w, lane);
+    vs.template store<false>(static_cast<uint4*>(a.v_out) + out, lo, hi, w, lane);
   }
 }
 

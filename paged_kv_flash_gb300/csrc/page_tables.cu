@@ -41,17 +41,21 @@ __device__ __forceinline__ int find_owner(const int32_t* cu, int lo, int hi, int
   return lo;
 }
 
-// The same for all lanes of a warp at once, 32 ways a round: three loads deep
-// for 32,768 requests where the binary search is fifteen.
-__device__ __forceinline__ int find_owner_warp(const int32_t* cu, int lo, int hi, int t, int lane) {
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) >> 5;
-    const int at = lo + lane * step;
-    const uint32_t m = __ballot_sync(0xffffffffu, at < hi && cu[at] <= t);    // a prefix of lanes
-    lo += (31 - __clz(m)) * step;
-    hi = min(hi, lo + step);
+// The owners of t0 and t1 among [0, hi), searched for side by side (the loads of
+// a round are independent).  All lanes of a warp load the same entry, and the
+// upper levels come from L1; 64 ways a round by different lanes was slower (32
+// lines a load).
+__device__ __forceinline__ int2 find_owners(const int32_t* cu, int hi, int t0, int t1) {
+  int l0 = 0, h0 = hi, l1 = 0, h1 = hi;
+  while (h0 - l0 > 1 || h1 - l1 > 1) {
+    const int m0 = l0 + ((h0 - l0) >> 1), m1 = l1 + ((h1 - l1) >> 1);
+    const bool up0 = cu[m0] <= t0, up1 = cu[m1] <= t1;
+    l0 = up0 ? m0 : l0;
+    h0 = up0 ? h0 : max(m0, l0 + 1);
+    l1 = up1 ? m1 : l1;
+    h1 = up1 ? h1 : max(m1, l1 + 1);
   }
-  return lo;
+  return make_int2(l0, l1);
 }
 
 __device__ __forceinline__ int checked(const pkv_host::TablesLaunch& a, int page) {
@@ -64,13 +68,15 @@ __device__ __forceinline__ int ring_at(const pkv_host::TablesLaunch& a, int head
   return (int)(at >= a.ring_capacity ? at - a.ring_capacity : at);
 }
 
-// The slot of position p of request b, which had `len` positions and takes its
-// pages from ring place `from` (counted from the ring's head).
-__device__ __forceinline__ int slot_of(const pkv_host::TablesLaunch& a, int b, int len, int head,
-                                       int from, int p) {
-  const int lp = p / kPageSize, held = pages_of(len);
-  const int page = checked(a, lp < held ? a.table[(size_t)b * a.max_pages + lp]
-                                        : a.ring[ring_at(a, head, from + lp - held)]);
+// The page of the lp-th of request b's pages, of which it had `held`; those it
+// takes start at ring place `from` (counted from the ring's head).
+__device__ __forceinline__ int page_of(const pkv_host::TablesLaunch& a, int b, int held, int head,
+                                       int from, int lp) {
+  return checked(a, lp < held ? a.table[(size_t)b * a.max_pages + lp]
+                              : a.ring[ring_at(a, head, from + lp - held)]);
+}
+
+__device__ __forceinline__ int slot_in(const pkv_host::TablesLaunch& a, int page, int p) {
   return page >= 0 && page < a.num_pages ? page * kPageSize + p % kPageSize : -1;
 }
 
@@ -116,47 +122,10 @@ __global__ void __launch_bounds__(kThreads)
     }
     return ok;
   };
-  // totals and checks first: a step that does not fit writes nothing
-  for (long long base = 0; base < a.batch; base += kTile) {
-    if (!load(base)) bad = 1;
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      long long sum = 0;
-#pragma unroll
-      for (int i = 0; i < kItems; ++i) sum += n[q][i];
-      if (small) {                                  // no sum can pass 31 bits
-        sum = __reduce_add_sync(FULL, (int)sum);
-      } else {
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
-      }
-      if (lane == 0 && sum)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&total[q]), (unsigned long long)sum);
-    }
-  }
-  __syncthreads();
-  const bool refuse =
-      bad || head < 0 || head >= cap || count < 0 || count > cap || total[1] > count ||
-      count + total[2] > cap || total[0] > 2147483647ll ||
-      (a.slots && total[0] > a.slot_capacity);
-  if (refuse) {
-    for (long long b = tid; b <= a.batch; b += kThreads) {
-      a.cu_new[b] = a.taken[b] = a.freed[b] = 0;
-      if (b < a.batch) a.seq_lens_out[b] = a.seq_lens[b];
-    }
-    if (tid == 0) {
-      a.ring_state_out[0] = head;
-      a.ring_state_out[1] = count;
-      atomicOr(&g_err_tables, kErrBadIndex);
-    }
-    return;
-  }
-
-  // prefix sums, a tile at a time (the only tile's counts are still here)
-  int32_t* const out[3] = {a.cu_new, a.taken, a.freed};
-  for (long long base = 0; base < a.batch; base += kTile) {
-    if (a.batch > kTile) load(base);
-    int v[3];
+  // inclusive sums over the tile: n within the thread, v up to it in its warp,
+  // wsum up to each warp
+  int v[3];
+  auto scan = [&]() {
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
 #pragma unroll
@@ -184,6 +153,55 @@ __global__ void __launch_bounds__(kThreads)
       wsum[warp][lane] = w;
     }
     __syncthreads();
+  };
+
+  // totals and checks first: a step that does not fit writes nothing.  A single
+  // tile whose sums cannot pass 31 bits has its totals from its scan.
+  const bool single = small && a.batch <= kTile;
+  if (single) {
+    if (!load(0)) bad = 1;
+    scan();
+    if (tid < 3) total[tid] = wsum[tid][31];
+  } else {
+    for (long long base = 0; base < a.batch; base += kTile) {
+      if (!load(base)) bad = 1;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        long long sum = 0;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) sum += n[q][i];
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
+        if (lane == 0 && sum)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&total[q]), (unsigned long long)sum);
+      }
+    }
+  }
+  __syncthreads();
+  const bool refuse =
+      bad || head < 0 || head >= cap || count < 0 || count > cap || total[1] > count ||
+      count + total[2] > cap || total[0] > 2147483647ll ||
+      (a.slots && total[0] > a.slot_capacity);
+  if (refuse) {
+    for (long long b = tid; b <= a.batch; b += kThreads) {
+      a.cu_new[b] = a.taken[b] = a.freed[b] = 0;
+      if (b < a.batch) a.seq_lens_out[b] = a.seq_lens[b];
+    }
+    if (tid == 0) {
+      a.ring_state_out[0] = head;
+      a.ring_state_out[1] = count;
+      atomicOr(&g_err_tables, kErrBadIndex);
+    }
+    return;
+  }
+
+  // prefix sums, a tile at a time
+  int32_t* const out[3] = {a.cu_new, a.taken, a.freed};
+  for (long long base = 0; base < a.batch; base += kTile) {
+    if (!single) {
+      load(base);
+      scan();
+    }
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
       const int before = carry[q] + (warp ? wsum[q][warp - 1] : 0) + v[q] - n[q][kItems - 1];
@@ -223,7 +241,9 @@ __global__ void __launch_bounds__(kThreads)
   if (a.slots)
     for (int t = tid; t < (int)total[0]; t += kThreads) {
       const int b = find_owner(s_cu[0], 0, B, t);
-      a.slots[t] = slot_of(a, b, s_len[b], head, s_cu[1][b], s_len[b] + (t - s_cu[0][b]));
+      const int p = s_len[b] + (t - s_cu[0][b]);
+      a.slots[t] = slot_in(
+          a, page_of(a, b, pages_of(s_len[b]), head, s_cu[1][b], p / kPageSize), p);
     }
   for (int i = tid; i < (int)total[1]; i += kThreads) {
     const int b = find_owner(s_cu[1], 0, B, i);
@@ -237,8 +257,8 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// The same for a large step, on the whole GPU.  A warp takes 512 consecutive
-// tokens, or 128 pages taken or freed: two searches by the warp bound the
+// The same for a large step, on the whole GPU.  A warp takes 256 consecutive
+// tokens, or 64 pages taken or freed: a search by the warp bounds the
 // requests they belong to, so that each lane's own search is over those alone
 // (none where one request holds them all); four tokens a lane make a 16-byte
 // store.
@@ -248,8 +268,8 @@ __global__ void __launch_bounds__(kFillThreads)
   const int B = a.batch, cap = a.ring_capacity;
   const int tokens = a.slots ? a.cu_new[B] : 0, taken = a.taken[B], freed = a.freed[B];
   const int head_new = a.ring_state_out[0], count_new = a.ring_state_out[1];
-  const int head = (int)(((long long)head_new - taken + cap) % cap);            // before the step
-  const int tail = (int)(((long long)head_new + count_new - freed + cap) % cap);
+  const int head = head_new >= taken ? head_new - taken : head_new - taken + cap;   // before
+  const int tail = ring_at(a, head_new, count_new - freed);                         // the step
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * (kFillThreads / 32);
   const bool wide = (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
@@ -264,12 +284,14 @@ __global__ void __launch_bounds__(kFillThreads)
     const int size = kind == 0 ? kChunk : kPageChunk;
     const int base = (c - (kind == 0 ? 0 : (kind == 1 ? c_tokens : c_tokens + c_taken))) * size;
     const int end = (int)min((long long)total, (long long)base + size);
-    const int b0 = find_owner_warp(cu, 0, B, base, lane);
-    const int b1 = find_owner_warp(cu, b0, B, end - 1, lane) + 1;
+    const int2 owners = find_owners(cu, B, base, end - 1);
+    const int b0 = owners.x, b1 = owners.y + 1;
     if (kind == 0) {
       for (int t0 = base + 4 * lane; t0 < end; t0 += 128) {
+        // four tokens, of one page as a rule: it is read when it changes
         int b = find_owner(cu, b0, b1, t0);
-        int first = cu[b], next = cu[b + 1];
+        int first = cu[b], next = cu[b + 1], len = a.seq_lens_out[b] - (next - first);
+        int from = a.taken[b], lp = -1, page = -1;
         int slot[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -280,9 +302,16 @@ __global__ void __launch_bounds__(kFillThreads)
             b = find_owner(cu, b + 1, b1, t);
             first = cu[b];
             next = cu[b + 1];
+            len = a.seq_lens_out[b] - (next - first);                           // before the step
+            from = a.taken[b];
+            lp = -1;
           }
-          const int len = a.seq_lens_out[b] - (next - first);                   // before the step
-          slot[e] = slot_of(a, b, len, head, a.taken[b], len + (t - first));
+          const int p = len + (t - first);
+          if (p / kPageSize != lp) {
+            lp = p / kPageSize;
+            page = page_of(a, b, pages_of(len), head, from, lp);
+          }
+          slot[e] = slot_in(a, page, p);
         }
         if (wide && t0 + 4 <= end) {
           *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
