@@ -102,12 +102,17 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev: Optional[int] = None) -> int:
+    """The handle of the stream, or of the current one; dev: the device of the
+    call's tensors, which must be the current one (the kernels run there)."""
+    now = torch.cuda.current_device()
+    if dev is not None and dev != now:
+        raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{now}")
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(now)
 
 
 def _check(status: int, what: str):
@@ -115,25 +120,27 @@ def _check(status: int, what: str):
         raise PkvError(status, what)
 
 
-def _need(t: torch.Tensor, dtype, name: str):
+def _need(t: torch.Tensor, dtype, name: str, dev: Optional[int] = None):
+    """A contiguous CUDA tensor of that dtype, on device dev where one is given."""
     if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor, got "
                          f"{t.dtype} on {t.device} (contiguous={t.is_contiguous()})")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors of the call on cuda:{dev}")
 
 
-def _need_smooth(k_smooth: torch.Tensor):
-    _need(k_smooth, torch.float32, "k_smooth")
-    if k_smooth.numel() != HEAD_DIM:
-        raise ValueError(f"k_smooth: expected {HEAD_DIM} entries, got {k_smooth.numel()}")
+def _need_smooth(k_smooth: Optional[torch.Tensor], dev: Optional[int] = None):
+    if k_smooth is not None:
+        _need(k_smooth, torch.float32, "k_smooth", dev)
+        if k_smooth.numel() != HEAD_DIM:
+            raise ValueError(f"k_smooth: expected {HEAD_DIM} entries, got {k_smooth.numel()}")
 
 
-def _one_device(what: str, *tensors):
-    """The tensors of one call lie on the current device, where the kernels run
-    (a pointer of another device would fault there)."""
-    now = torch.cuda.current_device()
+def _on(dev: int, *tensors):
+    """What is given of the tensors lies on device dev."""
     for t in tensors:
-        if t is not None and t.get_device() != now:
-            raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{now}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor on {t.device}, other tensors of the call on cuda:{dev}")
 
 
 @dataclass
@@ -165,7 +172,7 @@ class Pool:
         loop makes many)."""
         k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
         key = (k.data_ptr(), v.data_ptr(), ks is not None and ks.data_ptr(),
-               vs is not None and vs.data_ptr(), k.shape, v.shape, k.dtype, k.device)
+               vs is not None and vs.data_ptr(), k.shape, v.shape, k.dtype, k.get_device())
         cached = self.__dict__.get("_c")
         if cached is None or cached[0] != key:
             self._validate()
@@ -225,18 +232,19 @@ class Pool:
 def kv_append(pool: Pool, k_new, v_new, cu_new, block_table, seq_lens, k_smooth=None,
               stream=None):
     """Write k_new/v_new [T][Hkv][128] bf16 into the pool (see pkv_kv_append)."""
-    _need(k_new, torch.bfloat16, "k_new")
-    _need(v_new, torch.bfloat16, "v_new")
-    for t, n in ((cu_new, "cu_new"), (block_table, "block_table"), (seq_lens, "seq_lens")):
-        _need(t, torch.int32, n)
-    if k_smooth is not None:
-        _need(k_smooth, torch.float32, "k_smooth")
+    dev = k_new.get_device()
+    _need(k_new, torch.bfloat16, "k_new", dev)
+    _need(v_new, torch.bfloat16, "v_new", dev)
+    _need(cu_new, torch.int32, "cu_new", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
+    _need_smooth(k_smooth, dev)
     pc = pool.c()
-    _one_device("kv_append", pool.k, k_new, v_new, cu_new, block_table, seq_lens, k_smooth)
+    _on(dev, pool.k)
     st = _lib.pkv_kv_append(ctypes.byref(pc), k_new.data_ptr(), v_new.data_ptr(), k_new.shape[0],
                             cu_new.data_ptr(), seq_lens.shape[0], block_table.data_ptr(),
                             block_table.shape[1], seq_lens.data_ptr(), _ptr(k_smooth),
-                            _stream(stream))
+                            _stream(stream, dev))
     _check(st, "pkv_kv_append")
 
 
@@ -245,26 +253,25 @@ def kv_unpack(src: Pool, dst: Pool, src_block_table, dst_block_table, seq_lens, 
     """Write positions starts[b] (0 if not given) .. seq_lens[b] - 1 of a 4-bit
     or INT8 pool into the bf16 pool dst, through a block table of each (see
     pkv_kv_unpack): what a prefill against a quantised prefix reads."""
-    for t, n in ((src_block_table, "src_block_table"), (dst_block_table, "dst_block_table"),
-                 (seq_lens, "seq_lens")):
-        _need(t, torch.int32, n)
+    dev = seq_lens.get_device()
+    _need(src_block_table, torch.int32, "src_block_table", dev)
+    _need(dst_block_table, torch.int32, "dst_block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
     B = seq_lens.shape[0]
     if src_block_table.shape[0] != B or dst_block_table.shape[0] != B:
         raise ValueError(f"kv_unpack: {B} sequences, but block tables of "
                          f"{src_block_table.shape[0]} and {dst_block_table.shape[0]} rows")
     if starts is not None:
-        _need(starts, torch.int32, "starts")
+        _need(starts, torch.int32, "starts", dev)
         if starts.numel() != B:
             raise ValueError(f"starts: expected {B} entries, got {starts.numel()}")
-    if k_smooth is not None:
-        _need_smooth(k_smooth)
+    _need_smooth(k_smooth, dev)
     sc, dc = src.c(), dst.c()
-    _one_device("kv_unpack", src.k, dst.k, src_block_table, dst_block_table, seq_lens, starts,
-                k_smooth)
+    _on(dev, src.k, dst.k)
     st = _lib.pkv_kv_unpack(ctypes.byref(sc), ctypes.byref(dc), B, src_block_table.data_ptr(),
                             src_block_table.shape[1], dst_block_table.data_ptr(),
                             dst_block_table.shape[1], _ptr(starts), seq_lens.data_ptr(),
-                            int(max_seq_len), _ptr(k_smooth), _stream(stream))
+                            int(max_seq_len), _ptr(k_smooth), _stream(stream, dev))
     _check(st, "pkv_kv_unpack")
 
 
@@ -276,7 +283,7 @@ def page_tables(seq_lens, new_lens, block_table, free_ring, ring_state, num_page
     [B][max_pages] for new_lens[b] tokens behind seq_lens[b]; new_lens[b] < 0
     frees request b's pages.  Without seq_lens_out / ring_state_out the state
     is updated in place.  All int32.  Returns (cu_new, seq_lens_out)."""
-    B = seq_lens.shape[0]
+    B, dev = seq_lens.shape[0], seq_lens.get_device()
     if seq_lens_out is None:
         seq_lens_out = seq_lens
     if ring_state_out is None:
@@ -289,22 +296,22 @@ def page_tables(seq_lens, new_lens, block_table, free_ring, ring_state, num_page
                         (ring_state, "ring_state", 2), (seq_lens_out, "seq_lens_out", B),
                         (ring_state_out, "ring_state_out", 2), (cu_new, "cu_new", B + 1),
                         (page_offsets, "page_offsets", 2 * (B + 1))):
+        _need(t, torch.int32, n, dev)
         if t.numel() != count:
             raise ValueError(f"{n}: expected {count} entries, got {t.numel()}")
-        _need(t, torch.int32, n)
-    _need(free_ring, torch.int32, "free_ring")
-    _need(block_table, torch.int32, "block_table")
+    _need(free_ring, torch.int32, "free_ring", dev)
+    _need(block_table, torch.int32, "block_table", dev)
     if slot_map is not None:
-        _need(slot_map, torch.int32, "slot_map")
+        _need(slot_map, torch.int32, "slot_map", dev)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table: expected [{B}][max_pages], got {tuple(block_table.shape)}")
-    _one_device("page_tables", seq_lens, new_lens, block_table, free_ring, ring_state, cu_new,
-                page_offsets, slot_map, seq_lens_out, ring_state_out)
     st = _lib.pkv_page_tables(
         seq_lens.data_ptr(), new_lens.data_ptr(), B, free_ring.data_ptr(), free_ring.numel(),
-        ring_state.data_ptr(), int(num_pages), block_table.data_ptr(), block_table.shape[1], seq_lens_out.data_ptr(),
+        ring_state.data_ptr(), int(num_pages), block_table.data_ptr(), block_table.shape[1],
+        seq_lens_out.data_ptr(),
         cu_new.data_ptr(), page_offsets.data_ptr(), _ptr(slot_map),
-        slot_map.numel() if slot_map is not None else 0, ring_state_out.data_ptr(), _stream(stream))
+        slot_map.numel() if slot_map is not None else 0, ring_state_out.data_ptr(),
+        _stream(stream, dev))
     _check(st, "pkv_page_tables")
     return cu_new, seq_lens_out
 
@@ -337,9 +344,10 @@ def paged_attn_decode(pool: Pool, q, block_table, seq_lens, max_seq_len, softmax
     fused=True merges the splits inside the split kernel
     (pkv_paged_attn_decode_fused; its workspace's counters must start zeroed,
     as decode_workspace() leaves them)."""
-    _need(q, torch.bfloat16, "q")
-    _need(block_table, torch.int32, "block_table")
-    _need(seq_lens, torch.int32, "seq_lens")
+    dev = q.get_device()
+    _need(q, torch.bfloat16, "q", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
     B, Hq, _ = q.shape
     if workspace is None:                   # (a given workspace's size is checked by the call)
         _, _, ws_bytes, zero_bytes = decode_plan(B, Hq, pool.num_kv_heads, max_seq_len,
@@ -350,15 +358,15 @@ def paged_attn_decode(pool: Pool, q, block_table, seq_lens, max_seq_len, softmax
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    _need_smooth(k_smooth, dev)
     pc = pool.c()
-    _one_device("paged_attn_decode", pool.k, q, block_table, seq_lens, k_smooth, workspace, out,
-                lse)
+    _on(dev, pool.k, workspace, out, lse)
     fn = _lib.pkv_paged_attn_decode_fused if fused else _lib.pkv_paged_attn_decode
     st = fn(
         ctypes.byref(pc), q.data_ptr(), B, Hq, block_table.data_ptr(), block_table.shape[1],
         seq_lens.data_ptr(), int(max_seq_len), float(softmax_scale), _ptr(k_smooth),
         int(num_splits), _ptr(workspace), workspace.numel() if workspace is not None else 0,
-        out.data_ptr(), _ptr(lse), _stream(stream))
+        out.data_ptr(), _ptr(lse), _stream(stream, dev))
     _check(st, "pkv_paged_attn_decode_fused" if fused else "pkv_paged_attn_decode")
     return out, lse
 
@@ -370,20 +378,22 @@ def paged_attn_decode_noalloc(pool: Pool, q, block_table, seq_lens, max_seq_len,
     partials live in the library's fixed 16 MiB device array instead of a
     workspace (see pkv_paged_attn_decode_noalloc).  Calls on one device share
     that array, so they must not overlap on the GPU."""
-    _need(q, torch.bfloat16, "q")
-    _need(block_table, torch.int32, "block_table")
-    _need(seq_lens, torch.int32, "seq_lens")
+    dev = q.get_device()
+    _need(q, torch.bfloat16, "q", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
     B, Hq, _ = q.shape
     if out is None:
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    _need_smooth(k_smooth, dev)
     pc = pool.c()
-    _one_device("paged_attn_decode_noalloc", pool.k, q, block_table, seq_lens, k_smooth, out, lse)
+    _on(dev, pool.k, out, lse)
     st = _lib.pkv_paged_attn_decode_noalloc(
         ctypes.byref(pc), q.data_ptr(), B, Hq, block_table.data_ptr(), block_table.shape[1],
         seq_lens.data_ptr(), int(max_seq_len), float(softmax_scale), _ptr(k_smooth),
-        int(num_splits), out.data_ptr(), _ptr(lse), _stream(stream))
+        int(num_splits), out.data_ptr(), _ptr(lse), _stream(stream, dev))
     _check(st, "pkv_paged_attn_decode_noalloc")
     return out, lse
 
@@ -425,7 +435,8 @@ def paged_attn_prefill(pool: Pool, q, cu_q, block_table, seq_lens, max_q_len, so
     pc = pool.c()
     st = _lib.pkv_paged_attn_prefill(
         ctypes.byref(pc), q.data_ptr(), T, cu_q.data_ptr(), seq_lens.shape[0], Hq,
-        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), int(max_q_len), float(softmax_scale),
+        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), int(max_q_len),
+        float(softmax_scale),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(num_ctas),
         out.data_ptr(), _ptr(lse), _stream(stream))
     _check(st, "pkv_paged_attn_prefill")
@@ -460,9 +471,11 @@ def paged_attn_decode_multi(pool: Pool, q, cu_q, block_table, seq_lens, max_q_le
     q [total_q][Hq][128] bf16 -> (out bf16, lse fp32), on a bf16 or a 4-bit
     pool (k_smooth: 4-bit pools only).  The workspace is allocated when not
     given."""
-    _need(q, torch.bfloat16, "q")
-    for t, n in ((cu_q, "cu_q"), (block_table, "block_table"), (seq_lens, "seq_lens")):
-        _need(t, torch.int32, n)
+    dev = q.get_device()
+    _need(q, torch.bfloat16, "q", dev)
+    _need(cu_q, torch.int32, "cu_q", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
     T, Hq, _ = q.shape
     B = seq_lens.shape[0]
     if workspace is None:
@@ -477,18 +490,17 @@ def paged_attn_decode_multi(pool: Pool, q, cu_q, block_table, seq_lens, max_q_le
     if k_smooth is not None:
         if pool.dtype != INT4:
             raise ValueError("k_smooth: the verify steps of 4-bit pools alone take it")
-        _need_smooth(k_smooth)
-    _one_device("paged_attn_decode_multi", pool.k, q, cu_q, block_table, seq_lens, k_smooth,
-                workspace, out, lse)
+        _need_smooth(k_smooth, dev)
+    _on(dev, pool.k, workspace, out, lse)
     int4 = pool.dtype == INT4
     fn = _lib.pkv_paged_attn_decode_multi_int4 if int4 else _lib.pkv_paged_attn_decode_multi
     st = fn(
         ctypes.byref(pc), q.data_ptr(), T, cu_q.data_ptr(), B, Hq, block_table.data_ptr(),
-        block_table.shape[1], seq_lens.data_ptr(), int(max_q_len), int(max_seq_len), float(softmax_scale),
+        block_table.shape[1], seq_lens.data_ptr(), int(max_q_len), int(max_seq_len),
+        float(softmax_scale),
         *((_ptr(k_smooth),) if int4 else ()), int(num_splits),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
-        _ptr(lse),
-        _stream(stream))
+        _ptr(lse), _stream(stream, dev))
     _check(st, "pkv_paged_attn_decode_multi_int4" if int4 else "pkv_paged_attn_decode_multi")
     return out, lse
 
@@ -511,7 +523,8 @@ def qkv_norm_rope_append(pool: Pool, qkv, num_q_heads, cu_new, block_table, seq_
         q_out = torch.empty((T, num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=qkv.device)
     pc = pool.c()
     st = _lib.pkv_qkv_norm_rope_append(
-        ctypes.byref(pc), qkv.data_ptr(), T, num_q_heads, _ptr(q_norm_w), _ptr(k_norm_w), float(eps),
+        ctypes.byref(pc), qkv.data_ptr(), T, num_q_heads, _ptr(q_norm_w), _ptr(k_norm_w),
+        float(eps),
         _ptr(rope_cos), _ptr(rope_sin), rope_cos.shape[0] if rope_cos is not None else 0,
         cu_new.data_ptr(), seq_lens.shape[0], block_table.data_ptr(), block_table.shape[1],
         seq_lens.data_ptr(), q_out.data_ptr(), _stream(stream))

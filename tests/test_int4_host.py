@@ -82,25 +82,34 @@ def test_binding_checks_4bit_pools(monkeypatch):
 
 
 def test_binding_refuses_tensors_of_another_device(monkeypatch):
-    """Every tensor of a call lies on the current device (the check alone: one
-    fake tensor of device 1 while device 0 is current)."""
+    """Every tensor of a call lies on one device, the current one (the checks
+    alone, on stand-ins for CUDA tensors)."""
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
 
     class T:
+        is_cuda, dtype = True, torch.int32
+
         def __init__(self, i):
             self.device = torch.device("cuda", i)
 
         def get_device(self):
             return self.device.index
 
-    pk._one_device("x", T(0), None, T(0))
+        def is_contiguous(self):
+            return True
+
+    pk._need(T(1), torch.int32, "x", 1)
+    pk._on(0, T(0), None, T(0))
     with pytest.raises(ValueError, match="cuda:1"):
-        pk._one_device("x", T(0), T(1))
+        pk._need(T(1), torch.int32, "x", 0)
+    with pytest.raises(ValueError, match="cuda:1"):
+        pk._on(0, T(0), T(1))
+    with pytest.raises(ValueError, match="current device"):
+        pk._stream(None, 1)
 
 
 def test_unpack_binding_refuses_mismatched_tables(monkeypatch):
     monkeypatch.setattr(pk, "_need", lambda *a: None)
-    monkeypatch.setattr(pk, "_one_device", lambda *a: None)
     src, dst = pk.Pool.empty(4, 2, dtype=torch.uint8, device="cpu"), pk.Pool.empty(4, 2, device="cpu")
     bt, lens = torch.zeros((2, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     for kw in (dict(a=bt[:1]), dict(b=bt[:1]), dict(starts=lens[:1]), dict(k_smooth=torch.ones(64))):
@@ -139,7 +148,6 @@ def test_page_tables_limits(lib):  # noqa: F811
 
 def test_page_tables_binding_checks_sizes(monkeypatch):
     monkeypatch.setattr(pk, "_need", lambda *a: None)
-    monkeypatch.setattr(pk, "_one_device", lambda *a: None)
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     good = dict(seq_lens=i(3), new_lens=i(3), block_table=i(3, 4), free_ring=i(9), ring_state=i(2),
                 num_pages=9)
@@ -200,7 +208,7 @@ def test_int4_verify_is_for_4bit_pools(lib):  # noqa: F811
 
 def test_verify_binding_refuses_weights_for_bf16_pools(monkeypatch):
     monkeypatch.setattr(pk, "_need", lambda *a: None)
-    monkeypatch.setattr(pk, "_stream", lambda s: None)
+    monkeypatch.setattr(pk, "_stream", lambda *a: None)
     q = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
     i = torch.zeros(2, dtype=torch.int32)
     ws = torch.zeros(256, dtype=torch.uint8)
