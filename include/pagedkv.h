@@ -93,7 +93,8 @@ typedef struct {
  *
  *  k_new, v_new  bf16 [num_tokens][num_kv_heads][128]; rows cu_new[b] ..
  *                cu_new[b+1]-1 belong to sequence b.
- *  cu_new        int32 [batch+1], non-decreasing, cu_new[batch] = num_tokens.
+ *  cu_new        int32 [batch+1], non-decreasing, cu_new[batch] <= num_tokens
+ *                (rows from cu_new[batch] on, a padded batch's, are left out).
  *  block_table   int32 [batch][max_pages] page ids.
  *  seq_lens      int32 [batch] cached positions of each sequence AFTER this
  *                append; new row i of sequence b goes to position
@@ -149,7 +150,8 @@ pkv_status pkv_decode_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_he
  *
  *  q            bf16 [batch][num_q_heads][128].
  *  block_table  int32 [batch][max_pages]; seq_lens int32 [batch] (device);
- *               max_seq_len (host) >= every seq_lens[b].
+ *               max_seq_len (host) >= every seq_lens[b] (INT4 pools: a length
+ *               past the plan's pages is flagged, the row covers those pages).
  *  k_smooth     INT8 and INT4 pools: the same fp32 [128] weight given to
  *               kv_append, or NULL if the keys were not smoothed; NULL for
  *               bf16.  INT4 pools: q and k_smooth 16-byte aligned, any number
@@ -346,7 +348,8 @@ pkv_status pkv_decode_multi_plan(int32_t batch, int32_t total_q, int32_t num_q_h
  * pkv_paged_attn_decode_multi_int4 -- and for max_q_len > 16).
  * A sequence with q_b > max_q_len, seq_lens[b] < q_b, a length past the
  * block table or a page id outside the pool is skipped and flagged for
- * pkv_poll_device_error.
+ * pkv_poll_device_error.  Rows from cu_q[batch] on (a padded batch's) are left
+ * as they were.
  */
 pkv_status pkv_paged_attn_decode_multi(const pkv_pool* pool, const void* q, int32_t total_q,
                                        const int32_t* cu_q, int32_t batch, int32_t num_q_heads,
@@ -402,7 +405,7 @@ pkv_status pkv_paged_attn_decode_multi_int4(const pkv_pool* pool, const void* q,
  *             rounded once.
  *  cu_new, block_table, max_pages, seq_lens: as pkv_kv_append; token i of
  *             sequence b sits at position seq_lens[b] - n_b + i (p < max_pos
- *             with RoPE).
+ *             with RoPE); rows from cu_new[batch] on are left out.
  *  q_out      bf16 [num_tokens][num_q_heads][128] (16-byte aligned).
  * The k heads (normed and rotated) and the v heads (copied) go to the new
  * tokens' pool slots.  bf16 pools only (PKV_ERR_UNSUPPORTED for INT8: append

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <iterator>
 #include <mutex>
 
 #include "common.cuh"
@@ -352,6 +353,25 @@ pkv_status pkv_page_tables(const int32_t* seq_lens, const int32_t* new_lens, int
   if (!seq_lens || !new_lens || !free_ring || !ring_state || !block_table || !seq_lens_out ||
       !cu_new || !page_offsets || !ring_state_out || (!slot_map && slot_capacity > 0))
     return PKV_ERR_INVALID;
+  // no two arrays overlap, but for the two states updated in place
+  struct Range {
+    const int32_t* at;
+    long long n;
+  };
+  const long long B = batch;
+  const Range r[] = {{seq_lens, B},
+                     {seq_lens_out == seq_lens ? nullptr : seq_lens_out, B},
+                     {ring_state, 2},
+                     {ring_state_out == ring_state ? nullptr : ring_state_out, 2},
+                     {new_lens, B},
+                     {cu_new, B + 1},
+                     {page_offsets, 2 * (B + 1)},
+                     {free_ring, ring_capacity},
+                     {block_table, B * max_pages},
+                     {slot_map, slot_capacity}};
+  for (const Range& x : r)
+    for (const Range* y = &x + 1; y < std::end(r); ++y)
+      if (x.at && y->at && x.at < y->at + y->n && y->at < x.at + x.n) return PKV_ERR_INVALID;
   pkv_host::TablesLaunch a{seq_lens,     new_lens,     batch,    free_ring,    ring_capacity,
                            ring_state,   num_pages,    block_table, max_pages, seq_lens_out,
                            cu_new,       page_offsets, page_offsets + (size_t)batch + 1,

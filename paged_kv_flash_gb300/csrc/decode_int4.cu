@@ -170,6 +170,13 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
   return v;
 }
 
+// The larger of two, the other one if one is NaN.
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t x, uint32_t y) {
+  const __half2 z = __hmax2(*reinterpret_cast<const __half2*>(&x),
+                            *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&x),
                             *reinterpret_cast<const __half2*>(&y));
@@ -296,7 +303,10 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   if (row0 >= R) return;
   const int npages = (L + kPageSize - 1) / kPageSize;
   if (split > 0 && p_begin >= npages) return;       // empty split: the merge skips it
-  const int nv = max(1, (npages + a.pages_per_split - 1) / a.pages_per_split);
+  // a length past the plan's: flagged, and the splits that there are merge
+  const int nv_all = max(1, (npages + a.pages_per_split - 1) / a.pages_per_split);
+  if (nv_all > a.splits && threadIdx.x == 0) atomicOr(&g_err_int4, kErrBadIndex);
+  const int nv = min(a.splits, nv_all);
   const bool direct = a.splits == 1 || nv == 1;
   const int p_end = min(npages, p_begin + a.pages_per_split);
   const int L_end = min(L, p_end * kPageSize);      // a step may reach past the split
@@ -508,17 +518,17 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
       vb[u] = *reinterpret_cast<const uint4*>(sc + qd * 32 + 16);
       if constexpr (CAREFUL) {
         const int left = L_end - (key0 + u * kPageSize + 4 * qd);   // valid slots from 4 qd on
-        if (left <= 0) va[u].x = va[u].y = 0u;
-        if (left <= 1) va[u].z = va[u].w = 0u;
-        if (left <= 2) vb[u].x = vb[u].y = 0u;
-        if (left <= 3) vb[u].z = vb[u].w = 0u;
-        vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(va[u].x, va[u].y), __vmaxu2(va[u].z, va[u].w)));
-        vm = __vmaxu2(vm, __vmaxu2(__vmaxu2(vb[u].x, vb[u].y), __vmaxu2(vb[u].z, vb[u].w)));
+        if (left > 0) vm = max_f16x2(vm, max_f16x2(va[u].x, va[u].y));
+        if (left > 1) vm = max_f16x2(vm, max_f16x2(va[u].z, va[u].w));
+        if (left > 2) vm = max_f16x2(vm, max_f16x2(vb[u].x, vb[u].y));
+        if (left > 3) vm = max_f16x2(vm, max_f16x2(vb[u].z, vb[u].w));
       }
     }
     if constexpr (CAREFUL) {
       // keep every V scale below 2^vexp (fp16 exponent field E: scale < 2^(E - 14))
-      vtop = max(vtop, __reduce_max_sync(FULL, (int)(max(vm & 0xffffu, vm >> 16) >> 10) - 14));
+      // (a NaN scale does not count: the rows that see its key become NaN anyway)
+      const uint32_t vmax = max(vm & 0xffffu, vm >> 16);
+      vtop = max(vtop, __reduce_max_sync(FULL, (int)((vmax & 0x7fffu) >> 10) - 14));
       if (vtop > vexp) raise_vexp(vtop);
     }
 
@@ -570,8 +580,21 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     // of one channel of each quad of both, the first group's P' in columns 0-3,
     // the second's in 4-7: as many MMAs for O, half as many for cs, half the
     // scaling of P.
+    // Slots that row r does not see (the causal edge, past the end) keep out of
+    // its sums whatever their scale is: 0 times a NaN would not.
+    int lim_r = 0;
+    if constexpr (CAREFUL) {
+      const int at0 = __shfl_sync(FULL, lim[0], r >> 1), at1 = __shfl_sync(FULL, lim[1], r >> 1);
+      lim_r = (r & 1) ? at1 : at0;
+    }
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;      // slots 4 qd, + 2; + 1, + 3
+      if constexpr (CAREFUL) {
+        const int last = lim_r - (key0 + u * kPageSize + 4 * qd);
+        keep0 = last >= 2 ? 0xffffffffu : (last >= 0 ? 0x0000ffffu : 0u);
+        keep1 = last >= 3 ? 0xffffffffu : (last >= 1 ? 0x0000ffffu : 0u);
+      }
       const uint32_t vcs = kst + u * kPageBytes + kInt4Slab;
 #pragma unroll
       for (int g2 = 0; g2 < 2; ++g2) {
@@ -580,8 +603,8 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
         const uint32_t sa0 = g2 ? va[u].y : va[u].x, sa1 = g2 ? vb[u].y : vb[u].x;
         const uint32_t sb0 = g2 ? va[u].w : va[u].z, sb1 = g2 ? vb[u].w : vb[u].z;
         if constexpr (four_rows(MODE)) {
-          const uint32_t pb0 = mul_f16x2(pw[u][0], __byte_perm(sa0, sa1, my_sel));
-          const uint32_t pb1 = mul_f16x2(pw[u][1], __byte_perm(sb0, sb1, my_sel));
+          const uint32_t pb0 = mul_f16x2(pw[u][0], __byte_perm(sa0, sa1, my_sel)) & keep0;
+          const uint32_t pb1 = mul_f16x2(pw[u][1], __byte_perm(sb0, sb1, my_sel)) & keep1;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t w0 = i ? vw[0] >> 8 : vw[0], w1 = i ? vw[1] >> 8 : vw[1];
@@ -597,8 +620,8 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
             const uint32_t w0 = vw[2 * w], w1 = vw[2 * w + 1];
             const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
             const uint32_t sel = w ? 0x7632u : 0x5410u;    // group g of two slots' words
-            const uint32_t pb0 = mul_f16x2(pw[u][0], __byte_perm(sa0, sa1, sel));
-            const uint32_t pb1 = mul_f16x2(pw[u][1], __byte_perm(sb0, sb1, sel));
+            const uint32_t pb0 = mul_f16x2(pw[u][0], __byte_perm(sa0, sa1, sel)) & keep0;
+            const uint32_t pb1 = mul_f16x2(pw[u][1], __byte_perm(sb0, sb1, sel)) & keep1;
             mma_f16(o[2 * g], w0 & NIB0, w0 & NIB1, w1 & NIB0, w1 & NIB1, pb0, pb1);
             mma_f16(o[2 * g + 1], x0 & NIB0, x0 & NIB1, x1 & NIB0, x1 & NIB1, pb0, pb1);
             mma_f16(cs[g2], w ? 0u : kEight, w ? kEight : 0u, w ? 0u : kEight, w ? kEight : 0u,

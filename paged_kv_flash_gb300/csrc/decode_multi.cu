@@ -436,7 +436,11 @@ __global__ void __launch_bounds__(128)
   const int bh = blockIdx.x;
   const int t = bh / a.num_q_heads;
   const int b = owner_seq(a.cu_q, a.batch, t);
+  const int q0 = a.cu_q[b], qn = a.cu_q[b + 1] - q0;
   int L = a.seq_lens[b];
+  // rows that the split kernel left out: those of a skipped sequence, those
+  // behind the last one
+  if (t - q0 >= qn || qn > a.max_q || L < qn) return;
   if (L < 0 || L > a.max_pages * kPageSize) L = 0;
   const int npages = (L + kPageSize - 1) / kPageSize;
   const int n = min(a.splits, (npages + a.pages_per_split - 1) / a.pages_per_split);

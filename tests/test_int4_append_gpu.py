@@ -126,6 +126,50 @@ def test_append_bad_page_is_flagged_and_skipped(pk):
     assert np.array_equal(pool.k.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8, torch.uint8])
+@pytest.mark.parametrize("counts", [[2, 0, 3], [0, 0, 0]])
+def test_rows_behind_the_last_sequence_are_left_out(pk, dtype, counts):
+    """A padded batch: the pool is the one that the rows of the sequences alone
+    leave, although the last one's table goes on."""
+    rng = np.random.default_rng(913)
+    lens = np.array([20, 7, 33], np.int32)
+    layout = W.scatter_pages(rng, lens + 16)
+    total = sum(counts)
+    kn = dev_bf16(W.normal_bf16(rng, (total + 9, 2, 128)))
+    pools = []
+    for n in (total, total + 9):
+        pool = pk.Pool.empty(layout.num_pages, 2, dtype=dtype)
+        for t in (pool.k, pool.v, pool.k_scale, pool.v_scale):
+            if t is not None:
+                t.zero_()
+        pk.kv_append(pool, kn[:n], kn[:n], dev(W.cu_from_counts(counts)),
+                     dev(layout.block_table), dev(lens))
+        assert pk.poll_device_error() == pk.OK
+        pools.append(pool)
+    for a, b in zip(*((p.k, p.v, p.k_scale, p.v_scale) for p in pools)):
+        assert a is None or torch.equal(a, b)
+    assert total == 0 or pools[1].k.float().abs().sum() > 0
+
+
+def test_fused_inputs_leave_out_rows_behind_the_last_sequence(pk):
+    rng = np.random.default_rng(914)
+    lens, counts = np.array([20, 7], np.int32), [2, 1]
+    layout = W.scatter_pages(rng, lens + 16)
+    qkv = dev_bf16(W.normal_bf16(rng, (8, 4 + 2 * 2, 128)))
+    pools, outs = [], []
+    for n in (3, 8):
+        pool = pk.Pool.empty(layout.num_pages, 2)
+        pool.k.zero_(), pool.v.zero_()
+        out = torch.full((n, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+        pk.qkv_norm_rope_append(pool, qkv[:n], 4, dev(W.cu_from_counts(counts)),
+                                dev(layout.block_table), dev(lens), q_out=out)
+        assert pk.poll_device_error() == pk.OK
+        pools.append(pool)
+        outs.append(out)
+    assert torch.equal(pools[0].k, pools[1].k) and torch.equal(pools[0].v, pools[1].v)
+    assert torch.equal(outs[0], outs[1][:3]) and (outs[1][3:] == 5).all()
+
+
 # ------------------------------------------------------------------- unpack
 
 def wide_layout(rng, lens, starts):

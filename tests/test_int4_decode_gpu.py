@@ -339,6 +339,90 @@ def test_step_longer_than_max_q_or_its_sequence_is_flagged(pk):
     assert pk.poll_device_error() == pk.OK
 
 
+@pytest.mark.parametrize("splits", [1, 3, 12])
+@pytest.mark.parametrize("G", [2, 8])
+def test_positions_a_row_does_not_see_may_hold_nan(pk, G, splits):
+    """NaN keys and values of the step's last two tokens reach the rows that see
+    them, and no earlier row."""
+    c = Case(2530 + G, [200, 77], 2 * G, 2, counts=[4, 5])
+    ro, rl, mag = c.ref()
+    for b in range(2):
+        for p in (c.lens[b] - 2, c.lens[b] - 1):
+            page = c.layout.block_table[b, p // 16]
+            for pool in (c.k, c.v):
+                scales_of(pool)[page].reshape(2, 16, 4)[:, p % 16] = np.nan
+    out, lse = c.multi(pk, splits)
+    early = [0, 1, 4, 5, 6]
+    close(out[early], ro[early], mag[early])
+    check_lse(lse[early], rl[early])
+    assert torch.isnan(out[[2, 3, 7, 8]]).all()
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_padded_and_skipped_rows_are_left_as_they_were(pk, many):
+    """Rows behind the last sequence, of a sequence without tokens and of a
+    skipped one; splits merged in clusters (few) and by the combine (many)."""
+    B = 80 if many else 3
+    counts = np.where(np.arange(B) % 3 == 1, 6, 3)
+    c = Case(2540, np.full(B, 300), 8, 2, counts=counts)
+    pool, _, bt, lens, ml = c.args(pk)
+    T = int(c.cu[-1])
+    q = torch.zeros((T + 7, 8, 128), dtype=torch.bfloat16, device="cuda")
+    q[:T] = dev_bf16(c.q)
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((T + 7, 8), 7.0, device="cuda")
+    pk.paged_attn_decode_multi(pool, q, dev(c.cu), bt, lens, 5, ml, SCALE, num_splits=8, out=out,
+                               lse=lse)
+    assert pk.poll_device_error() == pk.ERR_INVALID          # six tokens of at most five
+    skipped = torch.ones(T + 7, dtype=torch.bool)
+    for b in np.nonzero(counts <= 5)[0]:
+        skipped[c.cu[b]:c.cu[b + 1]] = False
+    assert (out[skipped.cuda()] == 7).all() and (lse[skipped.cuda()] == 7).all()
+    rows = np.nonzero(~skipped.numpy())[0][:30]
+    ro, rl, mag = c.ref()
+    close(out[torch.from_numpy(rows).cuda()], ro[rows], mag[rows])
+
+
+def test_bf16_padded_rows_are_left_as_they_were(pk):
+    rng = np.random.default_rng(2545)
+    lens = np.array([300, 200], np.int32)
+    layout = W.scatter_pages(rng, lens)
+    pool = pk.Pool(*(dev_bf16(W.normal_bf16(rng, (layout.num_pages, 2, 16, 128)))
+                     for _ in range(2)))
+    q = dev_bf16(W.normal_bf16(rng, (12, 8, 128)))
+    out = torch.full_like(q, 7.0)
+    args = (dev(W.cu_from_counts([3, 4])), dev(layout.block_table), dev(lens), 4, 300, SCALE)
+    pk.paged_attn_decode_multi(pool, q, *args, num_splits=4, out=out)
+    want, _ = pk.paged_attn_decode_multi(pool, q[:7].contiguous(), *args, num_splits=4)
+    assert pk.poll_device_error() == pk.OK
+    assert torch.equal(out[:7], want) and (out[7:] == 7).all()
+
+
+@pytest.mark.parametrize("splits", [1, 2, 8, 20])
+def test_lengths_past_the_plan_are_flagged(pk, splits):
+    """max_seq_len below a length that the block table still holds: an error, the
+    other sequences right, the next (fused) call right."""
+    c = Case(2550, [640, 320, 100], 8, 2)
+    pool, q, bt, lens, _ = c.args(pk)
+    ro, _, mag = c.ref()
+    _, _, wsb, zero = pk.decode_plan(3, 8, 2, 640, splits, pk.INT4)
+    ws = torch.zeros(max(wsb, 256), dtype=torch.uint8, device="cuda")
+    for fused in (False, True):
+        out, _ = pk.paged_attn_decode(pool, q, bt, lens, 320, SCALE, num_splits=splits,
+                                      workspace=ws, fused=fused)
+        assert pk.poll_device_error() == pk.ERR_INVALID
+        close(out[1:], ro[1:], mag[1:])
+        assert torch.isfinite(out).all()
+        out, _ = pk.paged_attn_decode(pool, q, bt, lens, 640, SCALE, num_splits=splits,
+                                      workspace=ws, fused=fused)
+        assert pk.poll_device_error() == pk.OK
+        close(out, ro, mag)
+    cu = dev(W.cu_from_counts([1, 1, 1]))
+    out, _ = pk.paged_attn_decode_multi(pool, q, cu, bt, lens, 1, 320, SCALE, num_splits=splits)
+    assert pk.poll_device_error() == pk.ERR_INVALID
+    close(out[1:], ro[1:], mag[1:])
+
+
 def test_append_decode_verify_run_together(pk):
     """A request's life on a 4-bit cache with smoothed keys: tables, append of
     the prompt, a verify step, then single tokens; each against float64."""

@@ -146,6 +146,20 @@ def test_page_tables_limits(lib):  # noqa: F811
     assert tables(lib, B=2147483647) == UNSUPPORTED
 
 
+def test_page_tables_refuses_arrays_that_overlap(lib):  # noqa: F811
+    """Each array a page apart, then each pair of them on one another; the two
+    states may be their own inputs, but not overlap them in part."""
+    names = ["lens", "new", "ring", "state", "bt", "out", "cu", "offs", "slots", "so"]
+    apart = {n: FAKE + 4096 * i for i, n in enumerate(names)}
+    for i, a in enumerate(names):
+        for b in names[i + 1:]:
+            if (a, b) in (("lens", "out"), ("state", "so")):
+                assert tables(lib, **{**apart, b: apart[a] + 4}) == INVALID
+            else:
+                assert tables(lib, **{**apart, b: apart[a]}) == INVALID
+    assert tables(lib, **{**apart, "cu": apart["bt"] + 4 * 31}) == INVALID       # its last entry
+
+
 def test_page_tables_binding_checks_sizes(monkeypatch):
     monkeypatch.setattr(pk, "_need", lambda *a: None)
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
