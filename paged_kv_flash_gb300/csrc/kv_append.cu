@@ -160,7 +160,7 @@ __device__ __forceinline__ uint32_t quantize_int4(const float (&x)[8], __half& s
 // writes 144 per vector pair.
 __global__ void __launch_bounds__(256) append_int4_kernel(pkv_host::AppendLaunch a) {
   const int lane = threadIdx.x & 31, i = lane & 15;
-  const long long rows = (long long)a.num_tokens * a.num_kv_heads;
+  const long long pairs = (((long long)a.num_tokens + 1) / 2) * a.num_kv_heads;
   const long long nwarps = ((long long)gridDim.x * blockDim.x) >> 5;
   uint8_t* __restrict__ kp = static_cast<uint8_t*>(a.k);
   uint8_t* __restrict__ vp = static_cast<uint8_t*>(a.v);
@@ -174,14 +174,16 @@ __global__ void __launch_bounds__(256) append_int4_kernel(pkv_host::AppendLaunch
     w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
   }
   // both halves of a warp run the loop together (the shuffles need them)
-  for (long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; 2 * pair < rows;
+  for (long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; pair < pairs;
        pair += nwarps) {
-    const long long row = 2 * pair + (lane >> 4);
-    const bool on = row < rows;
+    const int h = (int)(pair % a.num_kv_heads);
+    const long long t = 2 * (pair / a.num_kv_heads) + (lane >> 4);
+    const long long row = t * a.num_kv_heads + h;
+    const bool on = t < a.num_tokens;
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     const uint4 kr = on ? __ldg(kn + row * 16 + i) : none;
     const uint4 vr = on ? __ldg(vn + row * 16 + i) : none;
-    const long long fs = on ? slot_of_row(a, (int)(row / a.num_kv_heads)) : -1;
+    const long long fs = on ? slot_of_row(a, (int)t) : -1;
     float x[8] = {bf16lo(kr.x), bf16hi(kr.x), bf16lo(kr.y), bf16hi(kr.y),
                   bf16lo(kr.z), bf16hi(kr.z), bf16lo(kr.w), bf16hi(kr.w)};
     if (a.k_smooth) {
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(256) append_int4_kernel(pkv_host::AppendLaunch
                         bf16lo(vr.z), bf16hi(vr.z), bf16lo(vr.w), bf16hi(vr.w)};
     const uint32_t vc = quantize_int4(y, vs);
     if (fs < 0) continue;
-    const int h = (int)(row % a.num_kv_heads), slot = (int)(fs & 15), g = i >> 2;
+    const int slot = (int)(fs & 15), g = i >> 2;
     const size_t slab = ((size_t)(fs >> 4) * a.num_kv_heads + h) * kInt4Slab;
     const size_t code = slab + g * 256 + slot * 16 + (i & 3) * 4;
     *reinterpret_cast<uint32_t*>(kp + code) = kc;
@@ -215,7 +217,7 @@ cudaError_t launch_append(const AppendLaunch& a, int dtype, cudaStream_t s) {
   if (a.num_tokens == 0) return cudaSuccess;
   const int sms = sm_count();
   if (dtype == PKV_INT4) {
-    const long long warps = ((long long)a.num_tokens * a.num_kv_heads + 1) / 2;
+    const long long warps = (((long long)a.num_tokens + 1) / 2) * a.num_kv_heads;
     const long long blocks = (warps + 7) / 8;
     const int grid = (int)std::min<long long>(blocks, (long long)sms * 16);
     append_int4_kernel<<<grid, 256, 0, s>>>(a);
