@@ -6,8 +6,10 @@
 //
 // A 4-bit page of a head is 2 x 1,152 bytes, so HBM leaves an SM ~51 ns, some
 // 100 cycles, per page (6.8 TB/s over 152 SMs): the kernel is bound by the
-// instructions per page unless codes reach the tensor cores almost as they
-// lie in memory.  They do, as f16 subnormals: a 16-bit half whose low four
+// instructions per page (8 sequences of 32,768 positions, 8 KV heads: 57 us, 52
+// us from L2, 44.5 us at HBM's rate; 240 instructions a page, the ALU at 53 %
+// and the tensor pipe at 34 % of their peaks), and would be more so if codes did
+// not reach the tensor cores almost as they lie in memory.  They do, as f16 subnormals: a 16-bit half whose low four
 // bits are u = code + 8 and whose other bits are 0 is exactly u 2^-24, and one
 // with u in bits 4-7 is u 2^-20, so one AND per register turns two codes of a
 // 32-bit word into two f16 MMA operands; nothing is converted and no exponent
@@ -75,9 +77,10 @@ constexpr int kPlain = 0, kLowApart = 1, kLowBeside = 2, kPlainFour = 3;
 constexpr bool weighted(int mode) { return mode == kLowApart || mode == kLowBeside; }
 constexpr bool four_rows(int mode) { return mode == kLowBeside || mode == kPlainFour; }
 
-// Shared memory: the query's offset fragment and scale factors, then its B fragments (8 k-steps x 32 lanes x 8 bytes, twice with a
-// low part: in registers they would cost 16 or 32 of them, a CTA per SM,
-// against 4 or 8 loads a page), then the warps' rings.
+// Shared memory: the query's offset fragment and scale factors, then its B
+// fragments (8 k-steps x 32 lanes x 8 bytes, twice with a low part: in registers
+// they would cost 16 or 32 of them, a CTA per SM, against 4 or 8 loads a page),
+// then the warps' rings.
 constexpr int qfrag_bytes(int mode) { return 2048 * (mode == kLowApart ? 2 : 1); }
 constexpr int smem_of(int mode) { return 1024 + qfrag_bytes(mode) + W * kWarpBytes; }
 static_assert(kCtasPerSm * (smem_of(kLowApart) + 1024) <= 228 * 1024, "resident CTAs");
@@ -85,11 +88,11 @@ static_assert(kCtasPerSm * (smem_of(kLowApart) + 1024) <= 228 * 1024, "resident 
 // Where all CTAs of a call are resident at once, up to this many splits of a
 // (sequence, KV head, row group) run as one thread-block cluster and merge
 // through distributed shared memory: no partials in global memory and no second
-// launch (one sequence of 1,024 positions: 7.2 -> 6.1 us).  In larger calls a
+// launch (one sequence of 1,024 positions: 7.2 -> 6.2 us).  In larger calls a
 // cluster would hold the places of its finished splits until the last one is
 // done (64 sequences of 512..8,192 positions: 86 -> 106 us).
 constexpr int kClusterSplits = pkv_host::kInt4ClusterSplits;
-constexpr int kMergeAt = 4608;                      // the split's result, behind warp 0's parked one
+constexpr int kMergeAt = 4608;                      // the split's result, behind warp 0's
 static_assert(kMergeAt >= kRows * (kHeadDim + 2) * 4 &&
                   kMergeAt + kRows * (kHeadDim + 1) * 4 <= kWarpBytes, "both fit warp 0's ring");
 
@@ -196,7 +199,8 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
 template <int MODE>
 __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const float* w, float sign,
                                              int qd, uint32_t (&hi)[8][2],
-                                             uint32_t (&lo)[weighted(MODE) ? 8 : 1][2], uint32_t& off) {
+                                             uint32_t (&lo)[weighted(MODE) ? 8 : 1][2],
+                                             uint32_t& off) {
   float x[4][8];
   float top = 0.f;
 #pragma unroll
@@ -336,7 +340,8 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
           ids = 0;
         }
       }
-      const uint64_t at0 = (uint64_t)(uint32_t)__shfl_sync(FULL, ids, (j % kSteps) * NP) * page_stride;
+      const uint64_t at0 =
+          (uint64_t)(uint32_t)__shfl_sync(FULL, ids, (j % kSteps) * NP) * page_stride;
       const uint64_t at1 =
           (uint64_t)(uint32_t)__shfl_sync(FULL, ids, (j % kSteps) * NP + 1) * page_stride;
       const uint8_t* k0 = k_lane + at0;
@@ -369,8 +374,8 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     if (qd == 0) s_back[r] = back;
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-      qs[ks * 32 + lane] =
-          low ? make_uint2(lo[weighted(MODE) ? ks : 0][0], lo[weighted(MODE) ? ks : 0][1]) : make_uint2(hi[ks][0], hi[ks][1]);
+      const uint32_t(&part)[2] = low ? lo[weighted(MODE) ? ks : 0] : hi[ks];
+      qs[ks * 32 + lane] = make_uint2(part[0], part[1]);
       if constexpr (MODE == kLowApart) qs[(8 + ks) * 32 + lane] = make_uint2(lo[ks][0], lo[ks][1]);
     }
   }
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
       const uint32_t vcs = kst + u * kPageBytes + kInt4Slab;
 #pragma unroll
       for (int g2 = 0; g2 < 2; ++g2) {
-        uint32_t vw[4];              // slots 4 qd, 4 qd + 2 and + 1, + 3 of group 2 g2, then 2 g2 + 1
+        uint32_t vw[4];              // slots 4 qd, + 2 and + 1, + 3 of group 2 g2, then 2 g2 + 1
         ldsm_x4_t(vcs + g2 * 512 + ld_row, vw);
         const uint32_t sa0 = g2 ? va[u].y : va[u].x, sa1 = g2 ? vb[u].y : vb[u].x;
         const uint32_t sb0 = g2 ? va[u].w : va[u].z, sb1 = g2 ? vb[u].w : vb[u].z;
@@ -632,11 +637,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     }
   };
 
-  // The first step watches the V scales and leaves kMargin octaves for the
-  // others, whose P' stays finite unless a scale outgrows them and its key's p
-  // is near the top.  If O is not finite at the end, a second pass watches
-  // every step (a NaN in the cache costs that pass too).
-  // step j: waits for its copy, works on it and refills its buffer with step j + NB
+  // Step j: waits for its copy, works on it and refills its buffer with step j + NB.
   auto take = [&](int j, auto careful_tag) {
     asm volatile("cp.async.wait_group %0;" ::"n"(NB - 1) : "memory");
     __syncwarp();                                   // the other lanes' parts too
@@ -645,6 +646,10 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
     __syncwarp();
     issue(j + NB);
   };
+  // The first step watches the V scales and leaves kMargin octaves for the
+  // others, whose P' stays finite unless a scale outgrows them and its key's p
+  // is near the top.  If O is not finite at the end, a second pass watches
+  // every step (a NaN in the cache costs that pass too).
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     reset();

@@ -475,10 +475,8 @@ cudaError_t launch_decode_multi(const MultiLaunch& a, bool int4, cudaStream_t s)
   if (a.batch == 0 || a.total_q == 0) return cudaSuccess;
   const cudaError_t e = int4 ? launch_multi_int4(a, s) : launch_multi_bf16(a, s);
   if (e != cudaSuccess || a.splits == 1) return e;
-  if (int4 &&
-      int4_merges_itself(a.splits, int4_units(a.batch, a.num_kv_heads,
-                                              (long long)a.max_q * (a.num_q_heads / a.num_kv_heads))))
-    return e;
+  const long long rows = (long long)a.max_q * (a.num_q_heads / a.num_kv_heads);
+  if (int4 && int4_merges_itself(a.splits, int4_units(a.batch, a.num_kv_heads, rows))) return e;
   // placed while the split kernel's last CTAs run; waits for its partials
   return pkv_host::launch_dependent(decode_multi_combine_kernel, dim3(a.total_q * a.num_q_heads),
                                     dim3(128), s, a);

