@@ -193,8 +193,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
 // into [2^13, 2^14).  With key weights the channels are multiplied by the key weight
 // and lo holds what f16 leaves of them (hi + lo is good to 2^-22).  Without it a
 // bf16 query is exact in f16 down to 2^-30 of the row's maximum.  off: the B
-// fragment of -8 sum(q) of the four groups, f16 high parts in rows 0-3 and low
-// parts in rows 4-7 (good to 2^-22).  Returns the power of two that undoes the
+// fragment of -8 sum(q) of the four groups, f16 high parts in rows 0-3 and 16
+// times the low parts in rows 4-7 (which without the 16 would be f16 subnormals;
+// good to 2^-22).  Returns the power of two that undoes the
 // scaling.
 template <int MODE>
 __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const float* w, float sign,
@@ -256,7 +257,7 @@ __device__ __forceinline__ float query_frags(const __nv_bfloat16* q0, const floa
   const float c0 = (qd & 1) ? sum[2] : sum[0], c1 = (qd & 1) ? sum[3] : sum[1];
   const uint32_t ch = pack_f16x2(c0, c1);
   const float2 cf = halves(ch);
-  off = qd < 2 ? ch : pack_f16x2(c0 - cf.x, c1 - cf.y);
+  off = qd < 2 ? ch : pack_f16x2(16.f * (c0 - cf.x), 16.f * (c1 - cf.y));
   return __int_as_float((127 - sh) << 23);
 }
 
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
   float zero[4];                                    // opaque, so that they stay in registers
 #pragma unroll
   for (int j = 0; j < 4; ++j) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[j]));
+  const uint32_t off_unit = qd < 2 ? 0x3C003C00u : 0x2C002C00u;       // 1, or 1 / 16
   const uint32_t my_sel = r < 4 ? 0x5410u : 0x7632u;  // four rows: this column's group of a pair
   // slot order of the MMA rows: row i = slot 2 i, row 8 + i = slot 2 i + 1, so
   // that a lane's scales are 16 contiguous bytes
@@ -468,8 +470,8 @@ __global__ void __launch_bounds__(W * 32, kCtasPerSm)
       const uint4 both = *reinterpret_cast<const uint4*>(sc + r * 16);      // slots 2 r, 2 r + 1
       ks0[u] = make_uint2(both.x, both.y);
       ks1[u] = make_uint2(both.z, both.w);
-      mma_f16_new(s[u], (qd & 1) ? both.y : both.x, (qd & 1) ? both.w : both.z, 0u, 0u, off, 0u,
-                  zero);
+      mma_f16_new(s[u], mul_f16x2((qd & 1) ? both.y : both.x, off_unit),
+                  mul_f16x2((qd & 1) ? both.w : both.z, off_unit), 0u, 0u, off, 0u, zero);
     }
 #pragma unroll
     for (int g2 = 0; g2 < 2; ++g2) {
