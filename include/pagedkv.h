@@ -433,7 +433,8 @@ pkv_status pkv_qkv_norm_rope_append(const pkv_pool* pool, const void* qkv, int32
  *               dst a bf16 pool with as many KV heads, in other memory.
  *  src_block_table, dst_block_table  int32 [batch][src_max_pages] and
  *               [batch][dst_max_pages]; entries of pages that hold no position
- *               of the range are not read, so dst may be a small staging pool.
+ *               of the range are not read, so dst may be a small staging pool;
+ *               no page of dst stands for two source pages.
  *  starts       int32 [batch] or NULL (0): the first position of each
  *               sequence, e.g. the positions that an earlier call has unpacked.
  *  seq_lens     int32 [batch]; max_seq_len (host) >= every seq_lens[b] and
